@@ -442,6 +442,94 @@ w4_status fp4_gemm(const uint16_t* X, const uint8_t* Wp, const float* s2, int M,
                    int K, int dq_group, uint16_t* Y, void* workspace,
                    size_t workspace_bytes, w4_stream stream);
 
+/* ------------------------------------------------------------------------
+ * FP8: block-scaled 8-bit floating point ([Comparison] §7.1: FP8 for weights
+ * and activations; [Comparison] §2.2: one scale per group).  A code is e4m3: 1
+ * sign, 4 exponent and 3 mantissa bits, largest value 448, no infinity, NaN
+ * 0x7F and 0xFF.  Scales are fp32:
+ *   activations  one scale per token and 128 channels, sx [M, KB],
+ *                KB = ceil(K / 128)
+ *   weights      one scale per 128 x 128 block, sw [ceil(N / 128), KB]
+ *   s = fp32(max|v over the block| / 448) (1 if that is 0)
+ *   q = e4m3_rne(fp32(v / s))                           (IEEE divisions)
+ * Blocks start at row and channel 0; the last of a row or column may be
+ * shorter.  K % 16 == 0 everywhere.  A block that holds an infinity or a NaN
+ * gets the scale NaN and NaN codes, so every product with it is NaN.
+ *
+ * fp8_quantize_weights: B matrices of one shape, each with its own blocks
+ *   W   in   fp32 [B, N, K], 16-byte aligned
+ *   qw  out  e4m3 [B, N, K], 16-byte aligned
+ *   sw  out  fp32 [B, ceil(N / 128), KB]
+ * fp8_quantize_activations
+ *   X   in   bf16 [M, K], 16-byte aligned
+ *   qx  out  e4m3 [M, K], 16-byte aligned;  sx  out  fp32 [M, KB]           */
+w4_status fp8_quantize_weights(const float* W, int B, int N, int K, uint8_t* qw, float* sw,
+                               w4_stream stream);
+w4_status fp8_quantize_activations(const uint16_t* X, int M, int K, uint8_t* qx, float* sx,
+                                   w4_stream stream);
+
+/* RMS norm of the residual stream, with an 8-bit output:
+ *   r = X + residual                                             (fp32)
+ *   y = r * rsqrt(mean_k(r^2) + eps) * weight                    (fp32)
+ *   residual_out = bf16_rne(r), Y = bf16_rne(y),
+ *   (qy, sy) = codes and scales of y as fp8_quantize_activations defines them,
+ *   from the unrounded y
+ *   X             in   bf16 [M, K];  K <= 65536 (else W4_ERR_UNSUPPORTED)
+ *   residual      in   bf16 [M, K] or NULL (r = X)
+ *   weight        in   bf16 [K];  eps >= 0
+ *   residual_out  out  bf16 [M, K] or NULL; may be residual or X
+ *   Y             out  bf16 [M, K] or NULL
+ *   qy, sy        out  e4m3 [M, K], fp32 [M, KB]
+ * All arrays but sy are 16-byte aligned.                                    */
+w4_status fp8_add_rmsnorm(const uint16_t* X, const uint16_t* residual, const uint16_t* weight,
+                          float eps, int M, int K, uint16_t* residual_out, uint16_t* Y,
+                          uint8_t* qy, float* sy, w4_stream stream);
+
+/* Y[m,n] = bf16_rne( sum_j sx[m,j] sw[n/128,j] sum_{k in block j} qx[m,k] qw[n,k] ),
+ * j over the 128-channel blocks; fp32 sums (the products of two codes are
+ * exact).
+ *   qx, sx     in   e4m3 [M, K] (16-byte aligned), fp32 [M, KB]
+ *   qw, sw     in   e4m3 [N, K] (16-byte aligned), fp32 [ceil(N / 128), KB]
+ *   M, N       1..2^24
+ *   Y          out  bf16 [M, N]
+ *   workspace  at least fp8_gemm_workspace_bytes(M, N, K) bytes (0 for an
+ *              invalid shape), 256-byte aligned, ZEROED ONCE before its first
+ *              use; the call leaves its counters (the first 262144 bytes)
+ *              zeroed, so calls of any shape, and w4a16_gemm / nf4_gemm, may
+ *              share it as long as they are ordered on one stream.
+ * As in w4a16_gemm the weights (qw, sw) are constant model state: they are
+ * read before the kernel before this one on the stream has finished, and must
+ * not be written by it (fp8_quantize_weights directly before is fine).      */
+size_t fp8_gemm_workspace_bytes(int M, int N, int K);
+w4_status fp8_gemm(const uint8_t* qx, const float* sx, const uint8_t* qw, const float* sw, int M,
+                   int N, int K, uint16_t* Y, void* workspace, size_t workspace_bytes,
+                   w4_stream stream);
+
+/* A mixture-of-experts layer for a few tokens (decoding), with e4m3 experts:
+ *   l = X router^T (fp32); ids[t] = the top experts with the largest l[t],
+ *     largest first, the lowest index on ties, NaN below every number
+ *   weights[t,j] = exp(l[t,ids[t,j]] - max) / sum of exp(l - max) over all
+ *     experts, or over the chosen ones with renormalize
+ *   (xq, sx) = codes of X;  g, u = xq . w13[e,0]^T, xq . w13[e,1]^T
+ *   h = g / (1 + exp(-g)) * u (fp32), (hq, sh) = codes of h
+ *   Y[t] = bf16_rne( sum_j weights[t,j] (hq . w2[ids[t,j]]^T) )
+ * with products, codes and scales as in fp8_gemm and fp8_quantize_activations.
+ *   X          in   bf16 [T, H], T <= 128;  router  in  bf16 [E, H], E <= 512
+ *   w13, s13   in   e4m3 [E, 2, I, H] (gate, up), fp32 [E, 2, ceil(I/128), ceil(H/128)]
+ *   w2, s2     in   e4m3 [E, H, I], fp32 [E, ceil(H/128), ceil(I/128)]
+ *              (fp8_quantize_weights with B = 2 E and B = E)
+ *   top        1..min(E, 16);  H, I multiples of 16, at most 2^20
+ *   Y          out  bf16 [T, H];  ids  out  int32 [T, top];  weights  out  fp32 [T, top]
+ *   workspace  as for fp8_gemm, fp8_moe_workspace_bytes(T, E, top, H, I) bytes
+ * T, E or top above the limits: W4_ERR_UNSUPPORTED.  X, router, w13, w2 are
+ * 16-byte aligned.  A token whose logits are all NaN is given experts
+ * 0..top-1 and a NaN output.                                                */
+size_t fp8_moe_workspace_bytes(int T, int E, int top, int H, int I);
+w4_status fp8_moe(const uint16_t* X, const uint16_t* router, const uint8_t* w13, const float* s13,
+                  const uint8_t* w2, const float* s2, int T, int E, int top, int H, int I,
+                  int renormalize, uint16_t* Y, int32_t* ids, float* weights, void* workspace,
+                  size_t workspace_bytes, w4_stream stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -11,3 +11,4 @@ generator (``weight_only_bit_gemm_b200.synthetic``), which draws random numbers
 and holds none of the quantization arithmetic.
 """
 from .w4_oracle import *  # noqa: F401,F403
+from .fp8_oracle import *  # noqa: F401,F403

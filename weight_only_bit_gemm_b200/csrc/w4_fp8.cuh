@@ -1,0 +1,237 @@
+// w4_fp8.cuh -- block-scaled 8-bit floating point (e4m3): quantization of
+// weights (one fp32 scale per 128 x 128 block) and activations (one per token
+// and 128 channels), and the residual RMS norm that writes its output in that
+// form.
+//
+//   s = max|v over the block| / 448   (IEEE division; 1 if that is 0)
+//   q = e4m3_rne(fp32(v / s))
+//
+// 448 is e4m3's largest value, so |v / s| <= 448 (1 + 2^-23) and nothing
+// saturates to anything but 448.  The maximum is taken on the bit patterns of
+// |v| as integers, whose order puts infinity and NaN above every finite value:
+// a block that holds one gets the scale NaN and NaN codes, so a product with
+// it is NaN instead of silently losing the value.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include <cstdint>
+
+#include "w4_ptx.cuh"
+
+namespace w4 {
+
+constexpr int kFp8Block = 128;       // channels (and weight rows) per scale
+constexpr float kFp8Max = 448.0f;    // largest e4m3 value
+
+// The scale of a block whose largest |v| has these bits.
+__device__ __forceinline__ float fp8_scale(uint32_t max_bits) {
+  if (max_bits >= 0x7F800000u) return __uint_as_float(0x7FC00000u);
+  const float s = __fdiv_rn(__uint_as_float(max_bits), kFp8Max);
+  return s == 0.0f ? 1.0f : s;
+}
+
+// Two e4m3 codes, the first in the low byte (round to nearest even).
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t d;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+
+// 8 bf16 values of a 16-byte load, widened.
+__device__ __forceinline__ void unpack_bf16x8(uint4 w, float (&v)[8]) {
+  const uint32_t p[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(p[i] << 16);
+    v[2 * i + 1] = __uint_as_float(p[i] & 0xFFFF0000u);
+  }
+}
+
+// Codes of 8 values: two words.
+__device__ __forceinline__ uint2 fp8_codes8(const float (&v)[8], float s) {
+  float q[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(v[i], s);
+  uint2 o;
+  o.x = e4m3x2(q[0], q[1]) | (e4m3x2(q[2], q[3]) << 16);
+  o.y = e4m3x2(q[4], q[5]) | (e4m3x2(q[6], q[7]) << 16);
+  return o;
+}
+
+// Largest |v| bits over the 16 lanes of this half warp.
+__device__ __forceinline__ uint32_t half_warp_max(uint32_t a) {
+#pragma unroll
+  for (int o = 1; o < 16; o <<= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
+  return a;
+}
+
+// ------------------------------------------------------------- activations
+// Half a warp per (token, 128 channels): 8 channels per lane, one 16-byte
+// load and one 8-byte store.  K % 16 == 0; lanes past K in a row's last block
+// hold nothing.
+__global__ void __launch_bounds__(256) fp8_quantize_x_kernel(const uint16_t* X, int M, int K,
+                                                             FastDivIdx by_kb, uint8_t* q,
+                                                             float* s) {
+  grid_dep_launch();
+  grid_dep_wait();
+  const int kb_n = (K + kFp8Block - 1) / kFp8Block;
+  const long long blocks = static_cast<long long>(M) * kb_n;
+  const int l = threadIdx.x & 15;
+  const long long step = static_cast<long long>(gridDim.x) * (blockDim.x / 16);
+  // every lane of a warp runs the same number of turns (the shuffles below)
+  const long long first = static_cast<long long>(blockIdx.x) * (blockDim.x / 16);
+  for (long long b0 = first; b0 < blocks; b0 += step) {
+    const long long b = b0 + threadIdx.x / 16;
+    const bool live = b < blocks;
+    const long long m = live ? static_cast<long long>(fast_div(static_cast<unsigned long long>(b), by_kb)) : 0;
+    const int kb = live ? static_cast<int>(b - m * kb_n) : 0;
+    const int k = kb * kFp8Block + l * 8;
+    const bool have = live && k < K;
+    float v[8] = {};
+    const size_t at = static_cast<size_t>(m) * K + k;
+    if (have) unpack_bf16x8(*reinterpret_cast<const uint4*>(X + at), v);
+    uint32_t mx = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) mx = max(mx, abs_bits(v[i]));
+    const float sc = fp8_scale(half_warp_max(mx));
+    if (have) *reinterpret_cast<uint2*>(q + at) = fp8_codes8(v, sc);
+    if (live && l == 0) s[b] = sc;
+  }
+}
+
+// ----------------------------------------------------------------- weights
+// One CTA per 128 x 128 block of one of B matrices: 16 lanes per row, 8
+// channels per lane, 16 rows at a time; the values stay in registers between
+// the maximum and the codes.
+__global__ void __launch_bounds__(256) fp8_quantize_w_kernel(const float* W, int N, int K,
+                                                             uint8_t* q, float* s) {
+  __shared__ uint32_t wmax[8];
+  const uint32_t kb_n = (K + kFp8Block - 1) / kFp8Block, nb_n = (N + kFp8Block - 1) / kFp8Block;
+  const uint32_t bn = blockIdx.x / kb_n, kb = blockIdx.x - bn * kb_n;
+  const uint32_t mat = bn / nb_n;
+  const int nb = static_cast<int>(bn - mat * nb_n);
+  const int l = threadIdx.x & 15, r0 = threadIdx.x >> 4;
+  const int k = static_cast<int>(kb) * kFp8Block + l * 8;
+  const float* Wm = W + static_cast<size_t>(mat) * N * K;
+  float v[8][8];
+  uint32_t mx = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int n = nb * kFp8Block + r0 + 16 * i;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+    if (n < N && k < K) {
+      const float4* p = reinterpret_cast<const float4*>(Wm + static_cast<size_t>(n) * K + k);
+      a = __ldcs(p);
+      b = __ldcs(p + 1);
+    }
+    v[i][0] = a.x; v[i][1] = a.y; v[i][2] = a.z; v[i][3] = a.w;
+    v[i][4] = b.x; v[i][5] = b.y; v[i][6] = b.z; v[i][7] = b.w;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) mx = max(mx, abs_bits(v[i][j]));
+  }
+  mx = half_warp_max(mx);
+  mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+  if ((threadIdx.x & 31) == 0) wmax[threadIdx.x >> 5] = mx;
+  __syncthreads();
+  mx = wmax[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) mx = max(mx, wmax[i]);
+  const float sc = fp8_scale(mx);
+  uint8_t* qm = q + static_cast<size_t>(mat) * N * K;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int n = nb * kFp8Block + r0 + 16 * i;
+    if (n < N && k < K)
+      *reinterpret_cast<uint2*>(qm + static_cast<size_t>(n) * K + k) = fp8_codes8(v[i], sc);
+  }
+  if (threadIdx.x == 0) s[blockIdx.x] = sc;
+  // a product launched next may read the weights before this grid has ended
+  __threadfence();
+}
+
+// ---------------------------------------------------------------- RMS norm
+// One CTA per token: r = x + residual in fp32 (kept in registers, 8 channels
+// per chunk, CPT chunks per thread), the mean of r^2 over the CTA, then
+// y = r * rsqrt(mean + eps) * w in fp32 and its codes without a rounding in
+// between.  residual_out is bf16(r); the norm itself uses the unrounded sum.
+// Every thread reads its own channels before it writes them, so residual_out
+// may be residual or x.
+template <int CPT>
+__global__ void __launch_bounds__(1024) fp8_add_rmsnorm_kernel(
+    const uint16_t* x, const uint16_t* residual, const uint16_t* __restrict__ weight, float eps,
+    int K, uint16_t* residual_out, uint16_t* y_out, uint8_t* q, float* s) {
+  __shared__ float part[32];
+  grid_dep_launch();
+  grid_dep_wait();
+  const size_t row = static_cast<size_t>(blockIdx.x) * K;
+  float v[CPT][8];
+  float ss = 0.0f;
+#pragma unroll
+  for (int c = 0; c < CPT; ++c) {
+    const int k = (static_cast<int>(threadIdx.x) + c * static_cast<int>(blockDim.x)) * 8;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[c][j] = 0.0f;
+    if (k < K) {
+      unpack_bf16x8(*reinterpret_cast<const uint4*>(x + row + k), v[c]);
+      if (residual) {
+        float r[8];
+        unpack_bf16x8(*reinterpret_cast<const uint4*>(residual + row + k), r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[c][j] += r[j];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ss = fmaf(v[c][j], v[c][j], ss);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+  const int warps = blockDim.x >> 5;
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = ss;
+  __syncthreads();
+  float total = 0.0f;
+  for (int w = 0; w < warps; ++w) total += part[w];
+  const float rstd = rsqrtf(total / static_cast<float>(K) + eps);
+  const int kb_n = (K + kFp8Block - 1) / kFp8Block;
+#pragma unroll
+  for (int c = 0; c < CPT; ++c) {
+    const int k = (static_cast<int>(threadIdx.x) + c * static_cast<int>(blockDim.x)) * 8;
+    const bool have = k < K;
+    if (have && residual_out) {
+      uint4 o;
+      uint32_t p[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        p[j] = static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(v[c][2 * j]))) |
+               (static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(v[c][2 * j + 1]))) << 16);
+      o.x = p[0]; o.y = p[1]; o.z = p[2]; o.w = p[3];
+      *reinterpret_cast<uint4*>(residual_out + row + k) = o;
+    }
+    float w8[8] = {};
+    if (have) unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(weight + k)), w8);
+    uint32_t mx = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      v[c][j] = v[c][j] * rstd * w8[j];
+      mx = max(mx, abs_bits(v[c][j]));
+    }
+    if (!have) mx = 0;  // 0 * rstd is NaN where rstd is not finite
+    mx = half_warp_max(mx);
+    if (!have) continue;
+    const float sc = fp8_scale(mx);
+    if (y_out) {
+      uint32_t p[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        p[j] = static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(v[c][2 * j]))) |
+               (static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(v[c][2 * j + 1]))) << 16);
+      *reinterpret_cast<uint4*>(y_out + row + k) = make_uint4(p[0], p[1], p[2], p[3]);
+    }
+    *reinterpret_cast<uint2*>(q + row + k) = fp8_codes8(v[c], sc);
+    if ((threadIdx.x & 15) == 0) s[static_cast<size_t>(blockIdx.x) * kb_n + k / kFp8Block] = sc;
+  }
+}
+
+}  // namespace w4

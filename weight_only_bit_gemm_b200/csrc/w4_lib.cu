@@ -9,8 +9,12 @@
 #include <cstdint>
 #include <cstring>
 #include <mutex>
+#include <type_traits>
 
 #include "../../include/w4.h"
+#include "w4_fp8.cuh"
+#include "w4_fp8_gemm.cuh"
+#include "w4_fp8_moe.cuh"
 #include "w4_gemm_kernel.cuh"
 #include "w4_gemv_kernel.cuh"
 #include "w4_gptq.cuh"
@@ -755,3 +759,4 @@ w4_status nf4_prepack(const uint8_t* Wq, const uint8_t* absmax_q, int N, int K, 
 }  // extern "C"
 
 #include "w4_gemm_host.inc"
+#include "w4_fp8_host.inc"

@@ -70,6 +70,13 @@ _SIGS = {
     "fp4_dequant": (_i, [_p, _p, _p, _i, _i, _i, _i, _p, _p]),
     "fp4_levels": (None, [_p]),
     "fp4_gemm": (_i, [_p, _p, _p, _i, _i, _i, _i, _p, _p, _sz, _p]),
+    "fp8_quantize_weights": (_i, [_p, _i, _i, _i, _p, _p, _p]),
+    "fp8_quantize_activations": (_i, [_p, _i, _i, _p, _p, _p]),
+    "fp8_add_rmsnorm": (_i, [_p, _p, _p, ctypes.c_float, _i, _i, _p, _p, _p, _p, _p]),
+    "fp8_gemm_workspace_bytes": (_sz, [_i, _i, _i]),
+    "fp8_gemm": (_i, [_p, _p, _p, _p, _i, _i, _i, _p, _p, _sz, _p]),
+    "fp8_moe_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
+    "fp8_moe": (_i, [_p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _p, _p, _p, _p, _sz, _p]),
 }
 def _bind(handle):
     for name, (res, args) in _SIGS.items():
@@ -505,3 +512,162 @@ def nf4_gemm(X, Wp, s2, N, K, dq_group=256, out=None, workspace=None):
 def fp4_gemm(X, Wp, s2, N, K, dq_group=256, out=None, workspace=None):
     """Y = X . w_hat^T for FP4 weights prepacked with nf4_prepack."""
     return _blockwise_gemm(lib.fp4_gemm, "fp4_gemm", X, Wp, s2, N, K, dq_group, out, workspace)
+
+
+# ----------------------------------------------------------------- FP8 (e4m3)
+
+FP8_BLOCK = 128
+
+
+def _blocks(n):
+    return (n + FP8_BLOCK - 1) // FP8_BLOCK
+
+
+def _fp8_arg(t, dtype, shape, device, name):
+    """A contiguous tensor of this type, shape and device (None dims: any)."""
+    if t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor on {device}")
+    if t.dim() != len(shape) or any(d is not None and d != n for d, n in zip(shape, t.shape)):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    return t
+
+
+def _fp8_out(out, dtype, shape, device, name):
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    return _fp8_arg(out, dtype, shape, device, name)
+
+
+def _fp8_device(t, name):
+    """The tensor's device, which has to be the current one (the stream is)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    return t.device
+
+
+_FP8_WS = {}
+_FP8_COUNTER_BYTES = 65536 * 4
+
+
+def _fp8_workspace(need, workspace, device):
+    """The caller's workspace, or one of this (device, stream), zeroed when it
+    is made.  A call that is being captured into a graph gets its own, zeroed
+    by the graph at each replay: graphs then share none."""
+    if workspace is not None:
+        _fp8_arg(workspace, torch.uint8, (None,), device, "workspace")
+        return _ws_view(workspace)
+    if torch.cuda.is_current_stream_capturing():
+        buf = torch.empty(need + 256, dtype=torch.uint8, device=device)
+        buf[:_FP8_COUNTER_BYTES + 256].zero_()
+        return _ws_view(buf)
+    key = (device.index, torch.cuda.current_stream().cuda_stream)
+    buf = _FP8_WS.get(key)
+    if buf is None or buf.numel() < need + 256:
+        buf = torch.zeros(max(need, 1 << 20) + 256, dtype=torch.uint8, device=device)
+        _FP8_WS[key] = buf
+    return _ws_view(buf)
+
+
+def fp8_quantize_weights(W):
+    """fp32 W [N, K] or [..., N, K] -> (e4m3 codes of W's shape, fp32 scales
+    [..., ceil(N/128), ceil(K/128)]), one scale per 128 x 128 block; K % 16 == 0."""
+    dev = _fp8_device(W, "W")
+    if W.dim() < 2:
+        raise ValueError("W must have at least two dimensions")
+    _cuda(W, torch.float32, "W")
+    N, K = W.shape[-2:]
+    B = W.numel() // (N * K) if N * K > 0 else 0
+    qw = torch.empty(W.shape, dtype=torch.float8_e4m3fn, device=dev)
+    sw = torch.empty(W.shape[:-2] + (_blocks(N), _blocks(K)), dtype=torch.float32, device=dev)
+    _check(lib.fp8_quantize_weights(_ptr(W), B, N, K, _ptr(qw), _ptr(sw), _stream()),
+           "fp8_quantize_weights")
+    return qw, sw
+
+
+def fp8_quantize_activations(X):
+    """bf16 X [M, K] -> (e4m3 codes [M, K], fp32 scales [M, ceil(K/128)]), one
+    scale per token and 128 channels; K % 16 == 0."""
+    dev = _fp8_device(X, "X")
+    _fp8_arg(X, torch.bfloat16, (None, None), dev, "X")
+    M, K = X.shape
+    qx = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=dev)
+    sx = torch.empty((M, _blocks(K)), dtype=torch.float32, device=dev)
+    _check(lib.fp8_quantize_activations(_ptr(X), M, K, _ptr(qx), _ptr(sx), _stream()),
+           "fp8_quantize_activations")
+    return qx, sx
+
+
+def fp8_add_rmsnorm(X, weight, residual=None, eps=1e-6, want_y=False, residual_out=None):
+    """r = X + residual, y = r * rsqrt(mean(r^2) + eps) * weight for bf16 X
+    [M, K] and weight [K]: (codes and scales of y as fp8_quantize_activations
+    gives them, bf16 r or None without a residual, bf16 y or None unless
+    want_y).  residual_out may be residual (in place)."""
+    dev = _fp8_device(X, "X")
+    _fp8_arg(X, torch.bfloat16, (None, None), dev, "X")
+    M, K = X.shape
+    _fp8_arg(weight, torch.bfloat16, (K,), dev, "weight")
+    if residual is not None:
+        _fp8_arg(residual, torch.bfloat16, (M, K), dev, "residual")
+        residual_out = _fp8_out(residual_out, torch.bfloat16, (M, K), dev, "residual_out")
+    elif residual_out is not None:
+        raise ValueError("residual_out without a residual")
+    y = torch.empty((M, K), dtype=torch.bfloat16, device=dev) if want_y else None
+    qy = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=dev)
+    sy = torch.empty((M, _blocks(K)), dtype=torch.float32, device=dev)
+    _check(lib.fp8_add_rmsnorm(_ptr(X), _ptr(residual), _ptr(weight), float(eps), M, K,
+                               _ptr(residual_out), _ptr(y), _ptr(qy), _ptr(sy), _stream()),
+           "fp8_add_rmsnorm")
+    return qy, sy, residual_out, y
+
+
+def fp8_gemm(qx, sx, qw, sw, out=None, workspace=None):
+    """bf16 Y[M, N] = (qx sx) . (qw sw)^T for codes and scales as
+    fp8_quantize_activations / fp8_add_rmsnorm and fp8_quantize_weights give them."""
+    dev = _fp8_device(qx, "qx")
+    _fp8_arg(qx, torch.float8_e4m3fn, (None, None), dev, "qx")
+    M, K = qx.shape
+    _fp8_arg(qw, torch.float8_e4m3fn, (None, K), dev, "qw")
+    N = qw.shape[0]
+    _fp8_arg(sx, torch.float32, (M, _blocks(K)), dev, "sx")
+    _fp8_arg(sw, torch.float32, (_blocks(N), _blocks(K)), dev, "sw")
+    out = _fp8_out(out, torch.bfloat16, (M, N), dev, "out")
+    need = lib.fp8_gemm_workspace_bytes(M, N, K)
+    if need == 0:
+        raise W4Error(W4_ERR_INVALID_ARG, "fp8_gemm_workspace_bytes")
+    ws = _fp8_workspace(need, workspace, dev)
+    _check(lib.fp8_gemm(_ptr(qx), _ptr(sx), _ptr(qw), _ptr(sw), M, N, K, _ptr(out), _ptr(ws),
+                        ws.numel(), _stream()), "fp8_gemm")
+    return out
+
+
+def fp8_moe(X, router, w13, s13, w2, s2, top_k, renormalize=True, out=None, workspace=None):
+    """A mixture-of-experts layer for up to 128 tokens: bf16 X [T, H], bf16
+    router [E, H], gate and up weights w13 [E, 2, I, H] and down weights w2
+    [E, H, I] with their scales as fp8_quantize_weights gives them ->
+    (bf16 Y [T, H], int32 expert ids [T, top_k], their fp32 weights [T, top_k])."""
+    dev = _fp8_device(X, "X")
+    _fp8_arg(X, torch.bfloat16, (None, None), dev, "X")
+    T, H = X.shape
+    _fp8_arg(router, torch.bfloat16, (None, H), dev, "router")
+    E = router.shape[0]
+    _fp8_arg(w13, torch.float8_e4m3fn, (E, 2, None, H), dev, "w13")
+    I = w13.shape[2]
+    _fp8_arg(s13, torch.float32, (E, 2, _blocks(I), _blocks(H)), dev, "s13")
+    _fp8_arg(w2, torch.float8_e4m3fn, (E, H, I), dev, "w2")
+    _fp8_arg(s2, torch.float32, (E, _blocks(H), _blocks(I)), dev, "s2")
+    out = _fp8_out(out, torch.bfloat16, (T, H), dev, "out")
+    need = lib.fp8_moe_workspace_bytes(T, E, top_k, H, I)
+    if need == 0:
+        supported = T <= 128 and E <= 512 and top_k <= 16
+        raise W4Error(W4_ERR_INVALID_ARG if supported else W4_ERR_UNSUPPORTED,
+                      "fp8_moe_workspace_bytes")
+    ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+    weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+    ws = _fp8_workspace(need, workspace, dev)
+    _check(lib.fp8_moe(_ptr(X), _ptr(router), _ptr(w13), _ptr(s13), _ptr(w2), _ptr(s2), T, E,
+                       top_k, H, I, int(bool(renormalize)), _ptr(out), _ptr(ids), _ptr(weights),
+                       _ptr(ws), ws.numel(), _stream()), "fp8_moe")
+    return out, ids, weights
