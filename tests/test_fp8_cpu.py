@@ -112,3 +112,60 @@ def test_workspace_sizes():
 def test_host_tensors_refused(call):
     with pytest.raises(ValueError, match="CUDA"):
         call(torch.zeros(16, 16, dtype=torch.bfloat16))
+
+
+# ------------------------------------- the matrix product's split of the work
+
+def plan(M, N, K, sms=148):
+    """The library's split (148 SMs is its count without a device)."""
+    pair = M > 128
+    ctas, nt = (2, 256) if pair else (1, 128)
+    p = dict(ctas=ctas, nt=nt, KB=-(-K // 128), workers=sms // ctas, rows=min(M, 128))
+    tiles = -(-M // (128 * ctas)) * -(-N // nt)
+    p["rounds"], p["tail"] = divmod(tiles, p["workers"])
+    p["runs"] = 0
+    units = p["tail"] * p["KB"]
+    if units:
+        runs = min(p["workers"], max(p["tail"], units // 4))
+        if -(-units // runs) + 6 < p["KB"]:
+            p["runs"] = runs
+    p["partial"] = 2 * p["runs"] * ctas * p["rows"] * nt
+    return p
+
+
+SHAPES = [(M, N, K) for M in (1, 7, 128, 129, 511, 2048, 8192)
+          for N, K in ((1, 16), (4096, 4096), (4096, 11008), (12288, 4096), (13824, 5120),
+                       (28672, 8192), (129, 28672), (20000, 512))]
+
+
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_product_split_covers_every_block_once(M, N, K):
+    p = plan(M, N, K)
+    L = w4.lib
+    assert L.fp8_gemm_workspace_bytes(M, N, K) == 65536 * 4 + -(-p["partial"] * 4 // 256) * 256
+    if not p["runs"]:
+        return
+    KB, U, G = p["KB"], p["tail"] * p["KB"], p["runs"]
+    assert p["tail"] <= G <= p["workers"]
+    start = [U * c // G for c in range(G + 1)]
+    pieces = {}                                   # tail tile -> [(run, k0, k1, slot)]
+    for c in range(G):
+        assert start[c] < start[c + 1]
+        u = start[c]
+        while u < start[c + 1]:
+            t, k0 = divmod(u, KB)
+            k1 = min(KB, k0 + start[c + 1] - u)
+            pieces.setdefault(t, []).append((c, k0, k1, 2 * c + (start[c] < t * KB)))
+            u += k1 - k0
+    slots = [s for v in pieces.values() for _, k0, k1, s in v if (k0, k1) != (0, KB)]
+    assert len(set(slots)) == len(slots) and max(slots, default=0) < 2 * G
+    run_of = lambda v: ((v + 1) * G - 1) // U  # noqa: E731
+    for t in range(p["tail"]):
+        v = pieces[t]
+        assert v[0][1] == 0 and v[-1][2] == KB
+        assert all(a[2] == b[1] for a, b in zip(v, v[1:]))
+        # the reducer's walk: runs first..last, the first one's slot by where
+        # it starts, the others' first slots
+        first, last = run_of(t * KB), run_of(t * KB + KB - 1)
+        assert [a[0] for a in v] == list(range(first, last + 1))
+        assert [a[3] for a in v[1:]] == [2 * c for c in range(first + 1, last + 1)]

@@ -3,9 +3,17 @@
 // weighted sum.
 #pragma once
 
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
 #include "w4_fp8_gemm.cuh"
 
 namespace w4 {
+
+__device__ __forceinline__ float e4m3_f32(uint8_t c) {
+  const __half_raw h = __nv_cvt_fp8_to_halfraw(c, __NV_E4M3);
+  return __half2float(__half(h));
+}
 
 constexpr int kMoeMaxTokens = 128;
 constexpr int kMoeMaxExperts = 512;
