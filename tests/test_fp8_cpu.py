@@ -125,10 +125,13 @@ def plan(M, N, K, sms=148):
     p["rounds"], p["tail"] = divmod(tiles, p["workers"])
     p["runs"] = 0
     units = p["tail"] * p["KB"]
-    if units:
-        runs = min(p["workers"], max(p["tail"], units // 4))
-        if -(-units // runs) + 6 < p["KB"]:
-            p["runs"] = runs
+    best = p["KB"]
+    for runs in range(p["tail"] + 1, p["workers"] + 1):
+        if p["tail"] == 0 or runs > units:
+            break
+        cost = units / runs + 5 + p["rows"] * nt * 4 / 44000 * (1 + runs / p["tail"])
+        if cost < best:
+            best, p["runs"] = cost, runs
     p["partial"] = 2 * p["runs"] * ctas * p["rows"] * nt
     return p
 

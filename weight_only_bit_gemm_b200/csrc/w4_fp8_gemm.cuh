@@ -16,8 +16,8 @@
 // CTA pairs (cta_group::2) of 256 x 256 with each CTA staging half of each
 // operand.  A stage is one block of 128 channels: both operands arrive by TMA
 // as rows of 128 bytes in the 128-byte swizzle (channels and rows past the
-// end read as zero).  Warp 0 issues the copies, warp 1 the MMAs, 8 warps are
-// the epilogue (4 tensor-memory lane quadrants x 2 column halves).
+// end read as zero).  Warp 0 issues the copies, warp 1 the MMAs, warps 4..11
+// are the epilogue (4 tensor-memory lane quadrants x 2 column halves).
 //
 // Work: a persistent grid.  Each worker (CTA or pair) takes whole tiles while
 // every worker gets one; the tiles left over are cut along K into equal runs
@@ -27,6 +27,8 @@
 #pragma once
 
 #include <cuda_bf16.h>
+
+#include <type_traits>
 
 #include "w4_fp8.cuh"
 
@@ -45,10 +47,19 @@ struct Fp8Cfg {
   static constexpr int kWRows = NT / kCtas;  // weight rows this CTA stages
   static constexpr int kXStage = kFp8Rows * 128;
   static constexpr int kWStage = kWRows * 128;
-  static constexpr int kThreads = 64 + kFp8EpiWarps * 32;
+  static constexpr int kThreads = 128 + kFp8EpiWarps * 32;
+  // pairs: 128 running sums per epilogue thread; registers move to them from
+  // the first warpgroup: (104 + 2 * 200) * 128 = 168 * 384 threads
+  static constexpr bool kRegSplit = PAIR;
+  static constexpr int kLaunchRegs = 168, kFewRegs = 104, kManyRegs = 200;
+  static_assert(kFewRegs * 128 + kManyRegs * 256 <= kLaunchRegs * kThreads, "register shares");
   static constexpr int kCols = NT / 2;       // columns per epilogue thread
   static constexpr int kTmemCols = 2 * NT;
-  static constexpr int kSmemBytes = 1024 + STAGES * (kXStage + kWStage) + (2 * STAGES + 5) * 8 + 16;
+  // per epilogue warp, a box of 32 tokens x 64 outputs in bf16 (128-byte rows)
+  // in the 128-byte swizzle
+  static constexpr int kYWarp = 32 * 64 * 2;
+  static constexpr int kSmemBytes = 1024 + STAGES * (kXStage + kWStage) + kFp8EpiWarps * kYWarp +
+                                    (2 * STAGES + 5) * 8 + 16;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 };
 
@@ -65,7 +76,8 @@ struct Fp8GemmArgs {
   int tail;               // tiles left over, the last ones
   int tail_workers;       // runs they are cut into (0: each whole, one worker each)
   int rows;               // rows of a partial slot
-  int vec;                // Y rows take 16-byte stores
+  int vec_s;              // sx and sw rows are 16-byte aligned
+  int vec;                // Y rows are 16-byte aligned: tensor copies and vector stores
   int keep_w;             // weights are read by several token tiles: keep them in L2
   unsigned long long partial_floats;  // extent, for the bounds-checked build
 };
@@ -137,13 +149,15 @@ __device__ __forceinline__ uint32_t bf16_pack2(float lo, float hi) {
 template <class C>
 __global__ void __launch_bounds__(C::kThreads, 1)
     fp8_tc_gemm_kernel(const __grid_constant__ CUtensorMap xmap,
-                       const __grid_constant__ CUtensorMap wmap, const Fp8GemmArgs a) {
+                       const __grid_constant__ CUtensorMap wmap,
+                       const __grid_constant__ CUtensorMap ymap, const Fp8GemmArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* xs = smem;                                   // STAGES x kXStage
   uint8_t* ws = xs + C::STAGES * C::kXStage;            // STAGES x kWStage
-  uint64_t* full = reinterpret_cast<uint64_t*>(ws + C::STAGES * C::kWStage);  // landed (tx)
+  uint8_t* ys = ws + C::STAGES * C::kWStage;            // 8 x kYWarp
+  uint64_t* full = reinterpret_cast<uint64_t*>(ys + kFp8EpiWarps * C::kYWarp);  // landed (tx)
   uint64_t* empty = full + C::STAGES;                   // MMAs done reading (commit)
   uint64_t* tfull = empty + C::STAGES;                  // block sum ready (commit)  [2]
   uint64_t* tempty = tfull + 2;                         // block sum read (8 or 16 warps) [2]
@@ -187,6 +201,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   Fp8Work work(a, worker);
   Fp8Piece p;
 
+  if (C::kRegSplit && warp < 4) regs_dec<C::kFewRegs>();
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
@@ -259,114 +274,198 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       constexpr uint32_t idesc = idesc_e4m3_f32(C::kCtas * 128, C::NT);
-      int it = 0;
+      const uint64_t xd0 = smem_desc_sw128(smem_u32(xs)), wd0 = smem_desc_sw128(smem_u32(ws));
+      int s = 0, it = 0;
+      uint32_t phase = 0;
       bool ok = true;
       while (ok && work.next(p)) {
         for (int kb = p.k0; kb < p.k1; ++kb, ++it) {
-          const int s = it % C::STAGES, b = it & 1;
-          if (!mbar_wait(&full[s], (it / C::STAGES) & 1) ||
-              (it >= 2 && !mbar_wait(&tempty[b], ((it >> 1) - 1) & 1))) {
-            ok = false;
-            break;
-          }
+          const int b = it & 1;
+          ok = mbar_wait_warp(&full[s], phase) &&
+               (it < 2 || mbar_wait_warp(&tempty[b], ((it >> 1) - 1) & 1));
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t xa = smem_u32(xs + s * C::kXStage);
-          const uint32_t wa = smem_u32(ws + s * C::kWStage);
+          // descriptor addresses are in units of 16 bytes
+          const uint64_t xd = xd0 + static_cast<uint32_t>(s) * (C::kXStage >> 4);
+          const uint64_t wd = wd0 + static_cast<uint32_t>(s) * (C::kWStage >> 4);
+          const uint32_t d = tmem + b * C::NT;
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            if constexpr (C::PAIR)
-              mma_f8_ss_pair(tmem + b * C::NT, smem_desc_sw128(xa + kk * 32),
-                             smem_desc_sw128(wa + kk * 32), idesc, kk > 0 ? 1u : 0u);
-            else
-              mma_f8_ss(tmem + b * C::NT, smem_desc_sw128(xa + kk * 32),
-                        smem_desc_sw128(wa + kk * 32), idesc, kk > 0 ? 1u : 0u);
+            for (int kk = 0; kk < 4; ++kk) {
+              if constexpr (C::PAIR)
+                mma_f8_ss_pair(d, xd + 2 * kk, wd + 2 * kk, idesc, kk > 0 ? 1u : 0u);
+              else
+                mma_f8_ss(d, xd + 2 * kk, wd + 2 * kk, idesc, kk > 0 ? 1u : 0u);
+            }
+            if constexpr (C::PAIR) {
+              mma_commit_pair(&empty[s], kFp8PairMask);
+              mma_commit_pair(&tfull[b], kFp8PairMask);
+            } else {
+              mma_commit(&empty[s]);
+              mma_commit(&tfull[b]);
+            }
           }
-          if constexpr (C::PAIR) {
-            mma_commit_pair(&empty[s], kFp8PairMask);
-            mma_commit_pair(&tfull[b], kFp8PairMask);
-          } else {
-            mma_commit(&empty[s]);
-            mma_commit(&tfull[b]);
+          __syncwarp();
+          if (++s == C::STAGES) {
+            s = 0;
+            phase ^= 1;
           }
         }
       }
-      if constexpr (C::PAIR)
-        mma_commit_pair(done, kFp8PairMask);
-      else
-        mma_commit(done);
+      if (elect_one()) {
+        if constexpr (C::PAIR)
+          mma_commit_pair(done, kFp8PairMask);
+        else
+          mma_commit(done);
+      }
+      __syncwarp();
     }
-  } else {
+  } else if (warp >= 4) {
     // ------------------------------------------------------------ epilogue
+    if (C::kRegSplit) regs_inc<C::kManyRegs>();
     const int quad = warp & 3;                 // tensor-memory lanes 32 quad ..
-    const int half = (warp - 2) >> 2;          // columns half * NT/2 ..
+    const int half = (warp - 4) >> 2;          // columns half * NT/2 ..
     const int row = quad * 32 + lane;
     const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * C::kCols;
+    uint8_t* yw = ys + (warp - 4) * C::kYWarp;
     bool ok = true;  // after a wait gave up: go through the motions without waiting
     int it = 0;
+    // this warp has read accumulator buffer b
+    // (a pair: on the leader's barrier)
+    const uint32_t te0 = C::PAIR ? mapa_shared(smem_u32(&tempty[0]), 0) : smem_u32(&tempty[0]);
+    auto release = [&](int b) {
+      tc_fence_before();
+      __syncwarp();
+      if constexpr (C::PAIR)
+        mbar_arrive_cluster_lane0(te0 + 8 * b, lane);
+      else
+        mbar_arrive_lane0(te0 + 8 * b, lane);
+    };
+    // Scales, four blocks at a time and four ahead: a token's are contiguous, so
+    // the 32 lanes' loads touch 32 lines, and shared memory and L1 have one data
+    // path that the operands already fill; 16-byte loads make that a quarter.
+    const float *sxp = nullptr, *swp = nullptr;
+    int mt = 0, nt = 0;
+    float4 sx4, sw4;  // of the next group of four
+    auto scales = [&](int g) {
+      if (a.vec_s) {
+        sx4 = __ldg(reinterpret_cast<const float4*>(sxp + g));
+        sw4 = __ldg(reinterpret_cast<const float4*>(swp + g));
+      } else {
+        const int g1 = min(g + 1, a.KB - 1), g2 = min(g + 2, a.KB - 1), g3 = min(g + 3, a.KB - 1);
+        sx4 = make_float4(__ldg(sxp + g), __ldg(sxp + g1), __ldg(sxp + g2), __ldg(sxp + g3));
+        sw4 = make_float4(__ldg(swp + g), __ldg(swp + g1), __ldg(swp + g2), __ldg(swp + g3));
+      }
+    };
+    auto begin = [&](const Fp8Piece& q) {
+      work.tile_at(q.tile, mt, nt);
+      const int m = (mt * C::kCtas + static_cast<int>(rank)) * kFp8Rows + row;
+      const int nb = (nt * C::NT + half * C::kCols) / kFp8Block;
+      sxp = a.sx + static_cast<size_t>(min(m, a.M - 1)) * a.KB;
+      swp = a.sw + static_cast<size_t>(min(nb, a.NB - 1)) * a.KB;
+      scales(q.k0 & ~3);
+    };
     grid_dep_wait();
-    while (work.next(p)) {
-      int mt, nt;
-      work.tile_at(p.tile, mt, nt);
+    Fp8Piece nx;
+    bool have = work.next(nx);
+    if (have) begin(nx);
+    while (have) {
+      p = nx;
       const int m0 = (mt * C::kCtas + static_cast<int>(rank)) * kFp8Rows;
       const int rows = min(kFp8Rows, a.M - m0);  // may be <= 0 in a pair's second CTA
       const bool busy = quad * 32 < rows;
-      const int m = m0 + row, n0 = nt * C::NT + half * C::kCols;
-      const float* sxp = a.sx + static_cast<size_t>(min(m, a.M - 1)) * a.KB;
-      const float* swp = a.sw + static_cast<size_t>(min(n0 / kFp8Block, a.NB - 1)) * a.KB;
+      const int ntile = nt, n0 = nt * C::NT + half * C::kCols;
       float acc[C::kCols];
 #pragma unroll
       for (int j = 0; j < C::kCols; ++j) acc[j] = 0.0f;
-      float sx_next = __ldg(sxp + p.k0), sw_next = __ldg(swp + p.k0);
+      float f0 = 0.f, f1 = 0.f, f2 = 0.f, f3 = 0.f;  // scales of this block and the next ones
+      auto next_four = [&](int g) {
+        f0 = sx4.x * sw4.x;
+        f1 = sx4.y * sw4.y;
+        f2 = sx4.z * sw4.z;
+        f3 = sx4.w * sw4.w;
+        if (g + 4 < p.k1) scales(g + 4);
+      };
+      next_four(p.k0 & ~3);
+      for (int i = 0; i < (p.k0 & 3); ++i) {
+        f0 = f1;
+        f1 = f2;
+        f2 = f3;
+      }
+#pragma unroll 1
       for (int kb = p.k0; kb < p.k1; ++kb, ++it) {
+        const float f = f0;
         const int b = it & 1;
-        const float f = sx_next * sw_next;
-        const int kn = min(kb + 1, p.k1 - 1);
-        sx_next = __ldg(sxp + kn);
-        sw_next = __ldg(swp + kn);
-        if (ok && !__all_sync(0xffffffffu, mbar_wait(&tfull[b], (it >> 1) & 1))) ok = false;
+        if (ok) ok = mbar_wait_warp(&tfull[b], (it >> 1) & 1);
         tc_fence_after();
         if (busy) {
+          // the next 16 columns load while the last are added
           uint32_t v[2][16];
           tmem_ld16(taddr + b * C::NT, v[0]);
 #pragma unroll
           for (int c = 0; c < C::kCols / 16; ++c) {
             tmem_wait_ld16(v[c & 1]);
-            if (c + 1 < C::kCols / 16) tmem_ld16(taddr + b * C::NT + 16 * (c + 1), v[(c + 1) & 1]);
+            if (c + 1 < C::kCols / 16)
+              tmem_ld16(taddr + b * C::NT + 16 * (c + 1), v[(c + 1) & 1]);
+            else
+              release(b);
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-              acc[16 * c + j] = fmaf(f, __uint_as_float(v[c & 1][j]), acc[16 * c + j]);
+            for (int j = 0; j < 16; j += 2)
+              fma2(acc[16 * c + j], acc[16 * c + j + 1], f, v[c & 1][j], v[c & 1][j + 1]);
           }
+        } else {
+          release(b);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if constexpr (C::PAIR)
-            mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[b]), 0));  // the leader's
-          else
-            mbar_arrive(&tempty[b]);
-        }
+        f0 = f1;
+        f1 = f2;
+        f2 = f3;
+        if ((kb & 3) == 3 && kb + 1 < p.k1) next_four(kb + 1);
       }
+      // the next piece's first scales travel while this one's sums are stored
+      have = work.next(nx);
+      if (have) begin(nx);
       if (p.k0 == 0 && p.k1 == a.KB) {
-        if (row < rows) {
-          uint16_t* y = a.Y + static_cast<size_t>(m) * a.N + n0;
+        if (!busy) continue;
+        // through shared memory, 64 columns at a time: a thread's columns of its
+        // token, 16 bytes at a time, swizzled so that 8 lanes' stores meet 8
+        // different bank groups
 #pragma unroll
-          for (int c = 0; c < C::kCols / 8; ++c) {
-            const int n = n0 + 8 * c;
-            if (a.vec && n + 8 <= a.N) {
-              uint4 o;
-              o.x = bf16_pack2(acc[8 * c], acc[8 * c + 1]);
-              o.y = bf16_pack2(acc[8 * c + 2], acc[8 * c + 3]);
-              o.z = bf16_pack2(acc[8 * c + 4], acc[8 * c + 5]);
-              o.w = bf16_pack2(acc[8 * c + 6], acc[8 * c + 7]);
-              *reinterpret_cast<uint4*>(y + 8 * c) = o;
-            } else {
+        for (int h = 0; h < C::kCols / 64; ++h) {
+          if (n0 + 64 * h >= a.N) break;
+          if (lane == 0) bulk_wait_read();  // the last copy has left the box
+          __syncwarp();
 #pragma unroll
-              for (int j = 0; j < 8; ++j)
-                if (n + j < a.N)
-                  y[8 * c + j] = __bfloat16_as_ushort(__float2bfloat16_rn(acc[8 * c + j]));
+          for (int c = 0; c < 8; ++c) {
+            const float* s8 = acc + 64 * h + 8 * c;
+            uint4 o;
+            o.x = bf16_pack2(s8[0], s8[1]);
+            o.y = bf16_pack2(s8[2], s8[3]);
+            o.z = bf16_pack2(s8[4], s8[5]);
+            o.w = bf16_pack2(s8[6], s8[7]);
+            *reinterpret_cast<uint4*>(yw + lane * 128 + ((c ^ (lane & 7)) << 4)) = o;
+          }
+          if (a.vec) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_3d(&ymap, yw, n0 + 64 * h, m0 + quad * 32, 0);
+              bulk_commit();
             }
+          } else {
+            __syncwarp();
+            for (int r = 0; r < 32 && quad * 32 + r < rows; ++r) {
+              uint16_t* y = a.Y + static_cast<size_t>(m0 + quad * 32 + r) * a.N + n0 + 64 * h;
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                const int col = 32 * c + lane;
+                if (n0 + 64 * h + col < a.N)
+                  y[col] = *reinterpret_cast<const uint16_t*>(yw + r * 128 +
+                                                              (((col >> 3) ^ (r & 7)) << 4) + (col & 7) * 2);
+              }
+            }
+            __syncwarp();
           }
         }
         continue;
@@ -393,7 +492,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       }
       __threadfence();
       epi_sync();
-      if (threadIdx.x == 64) {
+      if (threadIdx.x == 128) {
         unsigned int* ctr = a.counter + tt * C::kCtas + static_cast<int>(rank);
         const unsigned prev = atom_add_acq_rel_gpu(ctr, 1u);
         const bool is_last = prev == static_cast<unsigned>(last - first);
@@ -409,35 +508,70 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         // runs after the first start inside this tile: their first slots
         const size_t s1 = ((static_cast<size_t>(first) * 2) * C::kCtas + rank) *
                           static_cast<size_t>(a.rows) * C::NT;
-        for (int e = static_cast<int>(threadIdx.x) - 64; e < rows * kQ; e += kFp8EpiWarps * 32) {
-          const int r = e / kQ, c4 = (e - r * kQ) * 4;
-          const size_t at = static_cast<size_t>(r) * C::NT + c4;
-          float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-          for (int c = first; c <= last; ++c) {
-            const size_t src = (c == first ? s0 : s1 + (c - first) * cstep) + at;
-            if (!in_bounds(src + 3, a.partial_floats)) continue;
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(a.partial + src));
-            sum.x += v.x;
-            sum.y += v.y;
-            sum.z += v.z;
-            sum.w += v.w;
-          }
-          const int n = nt * C::NT + c4;
-          uint16_t* y = a.Y + static_cast<size_t>(m0 + r) * a.N + n;
-          if (a.vec && n + 4 <= a.N) {
-            *reinterpret_cast<uint2*>(y) = make_uint2(bf16_pack2(sum.x, sum.y), bf16_pack2(sum.z, sum.w));
-          } else {
-            const float s4[4] = {sum.x, sum.y, sum.z, sum.w};
+        // loads in flight per L2 round trip: 8 runs of one element (few tokens)
+        // or 2 runs of 4 elements; the additions stay in the order of the runs
+        const int tid = static_cast<int>(threadIdx.x) - 128;
+        const int total = rows * kQ;
+        auto sum_of = [&](auto elems, auto runs, int e0) {
+          constexpr int kE = decltype(elems)::value, kR = decltype(runs)::value;
+          float4 sum[kE];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              if (n + j < a.N) y[j] = __bfloat16_as_ushort(__float2bfloat16_rn(s4[j]));
+          for (int j = 0; j < kE; ++j) sum[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+          for (int c = first; c <= last; c += kR) {
+            float4 v[kR][kE];
+#pragma unroll
+            for (int u = 0; u < kR; ++u) {
+              const size_t src = c + u == first ? s0 : s1 + (c + u - first) * cstep;
+#pragma unroll
+              for (int j = 0; j < kE; ++j) {
+                const int e = e0 + j * kFp8EpiWarps * 32;
+                const size_t at = src + static_cast<size_t>(e) * 4;
+                v[u][j] = c + u <= last && e < total && in_bounds(at + 3, a.partial_floats)
+                              ? __ldcg(reinterpret_cast<const float4*>(a.partial + at))
+                              : make_float4(0.f, 0.f, 0.f, 0.f);
+              }
+            }
+#pragma unroll
+            for (int u = 0; u < kR; ++u)
+#pragma unroll
+              for (int j = 0; j < kE; ++j) {
+                if (c + u > last) continue;
+                sum[j].x += v[u][j].x;
+                sum[j].y += v[u][j].y;
+                sum[j].z += v[u][j].z;
+                sum[j].w += v[u][j].w;
+              }
           }
+#pragma unroll
+          for (int j = 0; j < kE; ++j) {
+            const int e = e0 + j * kFp8EpiWarps * 32;
+            if (e >= total) break;
+            const int r = e / kQ, n = ntile * C::NT + (e - r * kQ) * 4;
+            uint16_t* y = a.Y + static_cast<size_t>(m0 + r) * a.N + n;
+            if (a.vec && n + 4 <= a.N) {
+              *reinterpret_cast<uint2*>(y) =
+                  make_uint2(bf16_pack2(sum[j].x, sum[j].y), bf16_pack2(sum[j].z, sum[j].w));
+            } else {
+              const float s4[4] = {sum[j].x, sum[j].y, sum[j].z, sum[j].w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (n + i < a.N) y[i] = __bfloat16_as_ushort(__float2bfloat16_rn(s4[i]));
+            }
+          }
+        };
+        if (total <= 2 * kFp8EpiWarps * 32) {
+          for (int e = tid; e < total; e += kFp8EpiWarps * 32)
+            sum_of(std::integral_constant<int, 1>{}, std::integral_constant<int, 8>{}, e);
+        } else {
+          for (int e = tid; e < total; e += 4 * kFp8EpiWarps * 32)
+            sum_of(std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{}, e);
         }
       }
     }
   }
 
+  if (warp >= 4 && lane == 0) bulk_wait_all();  // output copies are complete
   tc_fence_before();
   if constexpr (C::PAIR)
     cluster_sync();  // neither CTA leaves while the other may reach its memory
