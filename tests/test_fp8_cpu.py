@@ -117,26 +117,23 @@ def test_host_tensors_refused(call):
 # ------------------------------------- the matrix product's split of the work
 
 def plan(M, N, K, sms=148):
-    """The library's split (148 SMs is its count without a device)."""
-    pair = M > 128
-    ctas, nt = (2, 256) if pair else (1, 128)
-    p = dict(ctas=ctas, nt=nt, KB=-(-K // 128), workers=sms // ctas, rows=min(M, 128))
-    tiles = -(-M // (128 * ctas)) * -(-N // nt)
+    """The library's split above 128 tokens (148 SMs is its count without a device)."""
+    p = dict(KB=-(-K // 128), workers=sms // 2, runs=0)
+    tiles = -(-M // 256) * -(-N // 256)
     p["rounds"], p["tail"] = divmod(tiles, p["workers"])
-    p["runs"] = 0
     units = p["tail"] * p["KB"]
     best = p["KB"]
     for runs in range(p["tail"] + 1, p["workers"] + 1):
         if p["tail"] == 0 or runs > units:
             break
-        cost = units / runs + 5 + p["rows"] * nt * 4 / 44000 * (1 + runs / p["tail"])
+        cost = units / runs + 5 + 128 * 256 * 4 / 44000 * (1 + runs / p["tail"])
         if cost < best:
             best, p["runs"] = cost, runs
-    p["partial"] = 2 * p["runs"] * ctas * p["rows"] * nt
+    p["partial"] = 2 * p["runs"] * 2 * 128 * 256
     return p
 
 
-SHAPES = [(M, N, K) for M in (1, 7, 128, 129, 511, 2048, 8192)
+SHAPES = [(M, N, K) for M in (129, 256, 511, 2048, 8192)
           for N, K in ((1, 16), (4096, 4096), (4096, 11008), (12288, 4096), (13824, 5120),
                        (28672, 8192), (129, 28672), (20000, 512))]
 
@@ -145,6 +142,7 @@ SHAPES = [(M, N, K) for M in (1, 7, 128, 129, 511, 2048, 8192)
 def test_product_split_covers_every_block_once(M, N, K):
     p = plan(M, N, K)
     L = w4.lib
+    assert L.fp8_gemm_workspace_bytes(128, N, K) == 65536 * 4
     assert L.fp8_gemm_workspace_bytes(M, N, K) == 65536 * 4 + -(-p["partial"] * 4 // 256) * 256
     if not p["runs"]:
         return

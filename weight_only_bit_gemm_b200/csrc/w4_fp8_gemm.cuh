@@ -12,14 +12,18 @@
 // in one block of 128 weight rows), and few tokens cost nothing but idle
 // lanes, which a call bound by its weight stream has to spare.
 //
-// Tiles of 128 tokens x NT weight rows per CTA, or, for more than 128 tokens,
-// CTA pairs (cta_group::2) of 256 x 256 with each CTA staging half of each
-// operand.  A stage is one block of 128 channels: both operands arrive by TMA
-// as rows of 128 bytes in the 128-byte swizzle (channels and rows past the
-// end read as zero).  Warp 0 issues the copies, warp 1 the MMAs, warps 4..11
-// are the epilogue (4 tensor-memory lane quadrants x 2 column halves).
+// A stage is one block of 128 channels: both operands arrive by TMA as rows of
+// 128 bytes in the 128-byte swizzle (channels and rows past the end read as
+// zero).  One warp issues the copies, one the MMAs, the epilogue warps are the
+// used tensor-memory lane quadrants x 2 column halves.
 //
-// Work: a persistent grid.  Each worker (CTA or pair) takes whole tiles while
+// Up to 128 tokens (fp8_rows_gemm_kernel): one tile of all tokens x 128 weight
+// rows per cluster, whose CTAs take a K range each and add their sums over
+// distributed shared memory.
+//
+// More tokens (fp8_tc_gemm_kernel): CTA pairs (cta_group::2) of 256 tokens x
+// 256 weight rows, each CTA staging half of each operand, in a persistent
+// grid.  Each worker (CTA or pair) takes whole tiles while
 // every worker gets one; the tiles left over are cut along K into equal runs
 // of blocks, one per worker, whose fp32 partial sums the last run of a tile
 // to finish adds in the order of K (the result does not depend on which
@@ -584,6 +588,265 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       tmem_dealloc_pair(tmem, C::kTmemCols);
     else
       tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+// ------------------------------------------------------- up to 128 tokens
+// QUADS: tensor-memory lane quadrants in use (32 tokens each).  With fewer than
+// 4 the MMA's other rows are whatever follows the token rows in shared memory
+// (inside it: the weight stages), and their sums are never read.  Up to 64
+// tokens two CTAs fit on an SM, so that the next call's stream their first
+// weights while this one's finish.
+template <int QUADS_, int STAGES_>
+struct Fp8RowsCfg {
+  static constexpr int QUADS = QUADS_;
+  static constexpr int STAGES = STAGES_;
+  static constexpr int kXStage = QUADS * 32 * 128;
+  static constexpr int kWStage = 128 * 128;
+  // epilogue warps: those whose number modulo 4 is a used quadrant
+  static constexpr int kWarps = QUADS == 1 ? 5 : QUADS == 2 ? 6 : 10;
+  static constexpr int kThreads = kWarps * 32;
+  static constexpr int kProducer = QUADS == 1 ? 1 : QUADS == 2 ? 2 : 8;
+  static constexpr int kMma = kProducer + 1;
+  static constexpr int kMinBlocks = QUADS == 4 ? 1 : 2;
+  static constexpr int kEpiWarps = 2 * QUADS;
+  // row stride of the fp32 sums in shared memory: 16 bytes past 128 columns,
+  // so that 8 lanes' 16-byte stores of 8 rows meet different banks
+  static constexpr int kRow = 132;
+  static constexpr int kRing = STAGES * (kXStage + kWStage);
+  static constexpr int kSmemBytes = 1024 + kRing + (2 * STAGES + 5) * 8 + 16;
+  static_assert(QUADS * 32 * kRow * 4 <= kRing, "the sums reuse the ring");
+  static_assert(STAGES * kWStage >= 128 * 128, "the MMA's unused rows stay inside");
+  static_assert(kMinBlocks * (kSmemBytes + 1024) <= 228 * 1024, "shared memory");
+};
+
+struct Fp8RowsArgs {
+  const float* sx;  // [M, KB]
+  const float* sw;  // [NB, KB]
+  uint16_t* Y;      // bf16 [M, N]
+  int M, N, KB;
+  int splits;       // CTAs of a cluster: K ranges of a tile
+  int vec;          // Y rows are 8-byte aligned
+};
+
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t cluster_addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(cluster_addr)
+               : "memory");
+  return v;
+}
+
+template <class C>
+__global__ void __launch_bounds__(C::kThreads, C::kMinBlocks)
+    fp8_rows_gemm_kernel(const __grid_constant__ CUtensorMap xmap,
+                         const __grid_constant__ CUtensorMap wmap, const Fp8RowsArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* xs = smem;                         // STAGES x kXStage
+  uint8_t* ws = xs + C::STAGES * C::kXStage;  // STAGES x kWStage
+  float* sums = reinterpret_cast<float*>(smem);  // [tokens][kRow], once the ring is idle
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kRing);  // landed (tx)
+  uint64_t* empty = full + C::STAGES;         // MMAs done reading (commit)
+  uint64_t* tfull = empty + C::STAGES;        // block sum ready (commit)   [2]
+  uint64_t* tempty = tfull + 2;               // block sum read (epilogue)  [2]
+  uint64_t* done = tempty + 2;                // every MMA complete (commit)
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(done + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int nt = static_cast<int>(blockIdx.x) / a.splits;
+  const int rank = static_cast<int>(blockIdx.x) - nt * a.splits;  // the cluster's CTAs in order
+  const int k0 = static_cast<int>(static_cast<long long>(a.KB) * rank / a.splits);
+  const int k1 = static_cast<int>(static_cast<long long>(a.KB) * (rank + 1) / a.splits);
+  const int n = k1 - k0;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::STAGES; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&tfull[i], 1);
+      mbar_init(&tempty[i], C::kEpiWarps);
+    }
+    mbar_init(done, 1);
+    fence_barrier_init();
+    grid_dep_launch();
+  }
+  if (warp == C::kMma) {
+    tmem_alloc(tmem_holder, 256);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  const bool epi = (warp & 3) < C::QUADS && warp < 8;
+
+  if (warp == C::kProducer) {
+    if (lane == 0) {
+      prefetch_tensormap(&wmap);
+      prefetch_tensormap(&xmap);
+      const uint64_t pol_w = policy_evict_first();  // read once
+      const uint64_t pol_x = policy_evict_last();
+      const uint32_t bytes = C::kWStage + static_cast<uint32_t>(a.M) * 128u;
+      // the weights do not depend on the previous kernel
+      for (int i = 0; i < n && i < C::STAGES; ++i) {
+        mbar_arrive_expect_tx(&full[i], bytes);
+        tma_load_3d(ws + i * C::kWStage, &wmap, (k0 + i) * 128, nt * 128, 0, &full[i], pol_w);
+      }
+      grid_dep_wait();
+      int i = 0;
+      for (; i < n; ++i) {
+        const int s = i % C::STAGES;
+        if (i >= C::STAGES) {
+          if (!mbar_wait(&empty[s], ((i / C::STAGES) - 1) & 1)) break;
+          mbar_arrive_expect_tx(&full[s], bytes);
+          tma_load_3d(ws + s * C::kWStage, &wmap, (k0 + i) * 128, nt * 128, 0, &full[s], pol_w);
+        }
+        tma_load_3d(xs + s * C::kXStage, &xmap, (k0 + i) * 128, 0, 0, &full[s], pol_x);
+      }
+      // never leave with copies in flight
+      for (int j = i - 1; j >= 0 && j >= i - C::STAGES; --j)
+        mbar_wait(&full[j % C::STAGES], (j / C::STAGES) & 1);
+    }
+  } else if (warp == C::kMma) {
+    constexpr uint32_t idesc = idesc_e4m3_f32(128, 128);
+    const uint64_t xd0 = smem_desc_sw128(smem_u32(xs)), wd0 = smem_desc_sw128(smem_u32(ws));
+    int s = 0;
+    uint32_t phase = 0;
+    for (int i = 0; i < n; ++i) {
+      const int b = i & 1;
+      if (!mbar_wait_warp(&full[s], phase) ||
+          (i >= 2 && !mbar_wait_warp(&tempty[b], ((i >> 1) - 1) & 1)))
+        break;
+      tc_fence_after();
+      // descriptor addresses are in units of 16 bytes
+      const uint64_t xd = xd0 + static_cast<uint32_t>(s) * (C::kXStage >> 4);
+      const uint64_t wd = wd0 + static_cast<uint32_t>(s) * (C::kWStage >> 4);
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          mma_f8_ss(tmem + b * 128, xd + 2 * kk, wd + 2 * kk, idesc, kk > 0 ? 1u : 0u);
+        mma_commit(&empty[s]);
+        mma_commit(&tfull[b]);
+      }
+      __syncwarp();
+      if (++s == C::STAGES) {
+        s = 0;
+        phase ^= 1;
+      }
+    }
+    if (elect_one()) mma_commit(done);
+    __syncwarp();
+  } else if (epi) {
+    const int quad = warp & 3, half = warp >> 2;
+    const int row = quad * 32 + lane;
+    const bool busy = quad * 32 < a.M;
+    const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * 64;
+    const uint32_t te0 = smem_u32(&tempty[0]);
+    const float* sxp = a.sx + static_cast<size_t>(min(row, a.M - 1)) * a.KB + k0;
+    const float* swp = a.sw + static_cast<size_t>(nt) * a.KB + k0;
+    float acc[64];
+#pragma unroll
+    for (int j = 0; j < 64; ++j) acc[j] = 0.0f;
+    bool ok = true;  // after a wait gave up: go through the motions without waiting
+    float sw_next = __ldg(swp);
+    grid_dep_wait();
+    float sx_next = __ldg(sxp);
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+      const int b = i & 1, in = min(i + 1, n - 1);
+      const float f = sx_next * sw_next;
+      sx_next = __ldg(sxp + in);
+      sw_next = __ldg(swp + in);
+      if (ok) ok = mbar_wait_warp(&tfull[b], (i >> 1) & 1);
+      tc_fence_after();
+      if (busy) {
+        uint32_t v[2][16];
+        tmem_ld16(taddr + b * 128, v[0]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          tmem_wait_ld16(v[c & 1]);
+          if (c < 3) tmem_ld16(taddr + b * 128 + 16 * (c + 1), v[(c + 1) & 1]);
+          if (c == 3) {
+            tc_fence_before();
+            __syncwarp();
+            mbar_arrive_lane0(te0 + 8 * b, lane);
+          }
+#pragma unroll
+          for (int j = 0; j < 16; j += 2)
+            fma2(acc[16 * c + j], acc[16 * c + j + 1], f, v[c & 1][j], v[c & 1][j + 1]);
+        }
+      } else {
+        tc_fence_before();
+        mbar_arrive_lane0(te0 + 8 * b, lane);
+      }
+    }
+    // every MMA of this CTA has read its operands (the last block's sum is
+    // complete), so the ring takes the sums
+    if (ok && row < a.M) {
+      float* dst = sums + row * C::kRow + half * 64;
+#pragma unroll
+      for (int c = 0; c < 16; ++c)
+        *reinterpret_cast<float4*>(dst + 4 * c) =
+            make_float4(acc[4 * c], acc[4 * c + 1], acc[4 * c + 2], acc[4 * c + 3]);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  // the cluster's sums are in place (a single CTA: its own)
+  if (a.splits > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+  // each CTA adds its share of the columns over the K ranges, in order of K
+  {
+    const int q0 = 32 * rank / a.splits, q1 = 32 * (rank + 1) / a.splits;  // in units of 4 columns
+    const int w = q1 - q0;
+    const uint32_t mine = smem_u32(sums);
+    for (int e = threadIdx.x; e < a.M * w; e += C::kThreads) {
+      const int r = e / w, c = (q0 + e - r * w) * 4;
+      const uint32_t at = mine + static_cast<uint32_t>(r * C::kRow + c) * 4u;
+      float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (a.splits == 1) {
+        sum = *reinterpret_cast<const float4*>(sums + r * C::kRow + c);
+      } else {
+        float4 v[8];
+#pragma unroll
+        for (int p = 0; p < 8; ++p)
+          if (p < a.splits) v[p] = ld_cluster_f4(mapa_shared(at, p));
+#pragma unroll
+        for (int p = 0; p < 8; ++p)
+          if (p < a.splits) {
+            sum.x += v[p].x;
+            sum.y += v[p].y;
+            sum.z += v[p].z;
+            sum.w += v[p].w;
+          }
+      }
+      const int col = nt * 128 + c;
+      uint16_t* y = a.Y + static_cast<size_t>(r) * a.N + col;
+      if (a.vec && col + 4 <= a.N) {
+        *reinterpret_cast<uint2*>(y) = make_uint2(bf16_pack2(sum.x, sum.y), bf16_pack2(sum.z, sum.w));
+      } else {
+        const float s4[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (col + j < a.N) y[j] = __bfloat16_as_ushort(__float2bfloat16_rn(s4[j]));
+      }
+    }
+  }
+  if (a.splits > 1)
+    cluster_sync();  // no CTA leaves while another reads its sums
+  else
+    __syncthreads();
+  if (warp == C::kMma) {
+    mbar_wait(done, 0);  // every issued MMA has completed
+    tc_fence_after();
+    tmem_dealloc(tmem, 256);
   }
 }
 
