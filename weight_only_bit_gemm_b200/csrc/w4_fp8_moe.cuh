@@ -1,138 +1,590 @@
 // w4_fp8_moe.cuh -- a mixture-of-experts layer over block-scaled e4m3 experts
-// for a few tokens: routing, gate and up products, SiLU, down product and the
-// weighted sum.
+// for up to 128 tokens, in two kernels:
+//
+//   moe_route_kernel   router logits, the choice of experts and their weights,
+//                      the tokens' e4m3 codes, the list of active experts;
+//   moe_expert_kernel  gate and up products with SiLU and the codes of h, then
+//                      the down products with the weighted sum.
+//
+// With few tokens the layer reads every active expert's weights once and is
+// bound by that stream, so each weight tile meets all the tokens: they are the
+// MMA's 128 rows as in fp8_rows_gemm_kernel, and a token that did not choose
+// the expert is a lane whose sums are left out.  Nothing is gathered or sorted;
+// h has a row for every (active expert, token), of which the chosen ones are
+// written and used.
+//
+// The down product's weight is linear in the block sums, so a cluster runs over
+// the blocks of all active experts in one pass with the routing weight folded
+// into the block's scale, and an output is written once.
+//
+// The expert kernel's clusters take their work by a counter, the gate and up
+// part first.  A cluster that waits for h therefore waits for clusters that
+// already run, whatever else occupies the GPU.
 #pragma once
-
-#include <cuda_fp16.h>
-#include <cuda_fp8.h>
 
 #include "w4_fp8_gemm.cuh"
 
 namespace w4 {
 
-__device__ __forceinline__ float e4m3_f32(uint8_t c) {
-  const __half_raw h = __nv_cvt_fp8_to_halfraw(c, __NV_E4M3);
-  return __half2float(__half(h));
-}
-
 constexpr int kMoeMaxTokens = 128;
 constexpr int kMoeMaxExperts = 512;
 constexpr int kMoeMaxTop = 16;
+constexpr int kMoeCluster = 8;       // CTAs of an expert-kernel cluster
+constexpr int kMoeRouteTokens = 4;   // tokens per routing CTA
+constexpr int kMoeRouteExperts = 8;  // experts per routing CTA (a warp each)
+
+// Counters of a call, all zero between calls.
+struct MoeCounters {
+  unsigned int ticket;     // expert-kernel clusters started
+  unsigned int h_done;     // CTAs that have published their part of h
+  unsigned int left;       // expert-kernel clusters finished
+  unsigned int groups;     // token groups routed
+  unsigned int group[kMoeMaxTokens / kMoeRouteTokens];  // routing CTAs done per group
+};
 
 struct MoeArgs {
   const uint16_t* X;       // bf16 [T, H]
   const uint16_t* router;  // bf16 [E, H]
-  const uint8_t* w13;      // [E, 2, I, H]: gate, up
   const float* s13;        // [E, 2, IB, HB]
-  const uint8_t* w2;       // [E, H, I]
   const float* s2;         // [E, HB, IB]
   uint16_t* Y;             // bf16 [T, H]
   int32_t* ids;            // [T, top]
   float* weights;          // [T, top]
   uint8_t* xq;             // [T, H]
   float* sx;               // [T, HB]
-  float* h;                // [T * top, I]
-  uint8_t* hq;             // [T * top, I]
-  float* sh;               // [T * top, IB]
+  float* logits;           // [T, E]
+  int32_t* active;         // [0] their number, then their experts, ascending
+  float* wt;               // [A, T]: routing weight, -1 where the token did not choose the expert
+  uint8_t* hq;             // [A, T, I]
+  float* sh;               // [A, T, IB]
+  MoeCounters* cnt;
   int T, E, top, H, I, HB, IB, renorm;
+  int A;                   // most experts that can be active
+  int route_ctas;          // routing CTAs; the ones after them quantize X
+  int ksplit;              // K ranges of a gate and up tile
+  int vec;                 // Y rows are 8-byte aligned
 };
 
-// A logit's place in the order of the choice: NaN below every number.
-__device__ __forceinline__ float moe_key(float v) { return v == v ? v : -INFINITY; }
+// ------------------------------------------------------------------ routing
+// Order of the choice: larger logits first, NaN below every number, as an
+// unsigned key that is never 0.
+__device__ __forceinline__ uint32_t moe_key(float v) {
+  const uint32_t b = __float_as_uint(v == v ? v + 0.0f : -INFINITY);  // -0 counts as 0
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
 
-// One CTA per token: logits (a warp per expert), the `top` largest (ties: the
-// lowest index), their softmax weights, and the token's e4m3 codes.
-__global__ void __launch_bounds__(256) moe_route_simple_kernel(const MoeArgs a) {
-  __shared__ float logit[kMoeMaxExperts];
-  const int t = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint16_t* x = a.X + static_cast<size_t>(t) * a.H;
-  for (int e = warp; e < a.E; e += 8) {
-    const uint16_t* r = a.router + static_cast<size_t>(e) * a.H;
-    float d = 0.0f;
-    for (int k = lane; k < a.H; k += 32)
-      d = fmaf(__uint_as_float(static_cast<uint32_t>(x[k]) << 16),
-               __uint_as_float(static_cast<uint32_t>(r[k]) << 16), d);
-    for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-    if (lane == 0) logit[e] = d;
+// A CTA of 8 warps: 8 experts (one per warp) x 4 tokens of logits; the last CTA
+// of a token group chooses its experts, and the last group's CTA lists the
+// active ones.  The CTAs after route_ctas write the tokens' codes.
+__global__ void __launch_bounds__(256) moe_route_kernel(const MoeArgs a) {
+  __shared__ uint32_t flags[kMoeMaxExperts];
+  __shared__ int slot[kMoeMaxExperts];
+  __shared__ int last;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  grid_dep_launch();
+  grid_dep_wait();
+
+  if (static_cast<int>(blockIdx.x) >= a.route_ctas) {
+    // 16 lanes per (token, 128 channels)
+    const int b = (static_cast<int>(blockIdx.x) - a.route_ctas) * 16 + (threadIdx.x >> 4);
+    const int l = threadIdx.x & 15;
+    const bool live = b < a.T * a.HB;
+    const int m = live ? b / a.HB : 0, k = (b - m * a.HB) * kFp8Block + l * 8;
+    const bool have = live && k < a.H;
+    float v[8] = {};
+    const size_t at = static_cast<size_t>(m) * a.H + k;
+    if (have) unpack_bf16x8(*reinterpret_cast<const uint4*>(a.X + at), v);
+    uint32_t mx = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) mx = max(mx, abs_bits(v[i]));
+    const float sc = fp8_scale(half_warp_max(mx));
+    if (have) *reinterpret_cast<uint2*>(a.xq + at) = fp8_codes8(v, sc);
+    if (live && l == 0) a.sx[b] = sc;
+    return;
   }
+
+  const int eg = (a.E + kMoeRouteExperts - 1) / kMoeRouteExperts;  // CTAs of a token group
+  const int tg = static_cast<int>(blockIdx.x) / eg;
+  const int t0 = tg * kMoeRouteTokens;
+  const int e = (static_cast<int>(blockIdx.x) - tg * eg) * kMoeRouteExperts + warp;
+  if (e < a.E) {
+    float d[kMoeRouteTokens] = {};
+    const uint16_t* r = a.router + static_cast<size_t>(e) * a.H;
+#pragma unroll 4
+    for (int k = lane * 8; k < a.H; k += 256) {
+      float rv[8];
+      unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(r + k)), rv);
+#pragma unroll
+      for (int i = 0; i < kMoeRouteTokens; ++i) {
+        if (t0 + i >= a.T) break;
+        float xv[8];
+        unpack_bf16x8(*reinterpret_cast<const uint4*>(a.X + static_cast<size_t>(t0 + i) * a.H + k), xv);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) d[i] = fmaf(rv[j], xv[j], d[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kMoeRouteTokens; ++i) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) d[i] += __shfl_xor_sync(0xffffffffu, d[i], o);
+      if (lane == 0 && t0 + i < a.T) a.logits[static_cast<size_t>(t0 + i) * a.E + e] = d[i];
+    }
+  }
+  __threadfence();
   __syncthreads();
   if (threadIdx.x == 0) {
-    float lmax = 0.0f, all = 0.0f, chosen = 0.0f;
-    for (int j = 0; j < a.top; ++j) {
-      int best = -1;
-      for (int e = 0; e < a.E; ++e) {
-        bool used = false;
-        for (int i = 0; i < j; ++i) used |= a.ids[t * a.top + i] == e;
-        if (!used && (best < 0 || moe_key(logit[e]) > moe_key(logit[best]))) best = e;
-      }
-      if (j == 0) lmax = logit[best];
-      a.ids[t * a.top + j] = best;
-      chosen += expf(logit[best] - lmax);
-    }
-    for (int e = 0; e < a.E; ++e) all += expf(logit[e] - lmax);
-    for (int j = 0; j < a.top; ++j)
-      a.weights[t * a.top + j] =
-          expf(logit[a.ids[t * a.top + j]] - lmax) / (a.renorm ? chosen : all);
+    last = atom_add_acq_rel_gpu(&a.cnt->group[tg], 1u) == static_cast<unsigned>(eg - 1) ? 1 : 0;
+    if (last) a.cnt->group[tg] = 0u;
   }
-}
-
-// h = silu(gate) * up for one (token, choice): a warp per channel.
-__global__ void __launch_bounds__(256) moe_up_simple_kernel(const MoeArgs a) {
-  const int p = blockIdx.x, t = p / a.top, lane = threadIdx.x & 31;
-  const int e = a.ids[p];
-  const int i = blockIdx.y * 8 + (threadIdx.x >> 5);
-  if (i >= a.I) return;
-  float gu[2] = {0.0f, 0.0f};
-  for (int kb = 0; kb < a.HB; ++kb) {
-    float d[2] = {0.0f, 0.0f};
-    for (int k = kb * 128 + lane; k < min(a.H, kb * 128 + 128); k += 32) {
-      const float xv = e4m3_f32(a.xq[static_cast<size_t>(t) * a.H + k]);
-      for (int g = 0; g < 2; ++g)
-        d[g] = fmaf(xv, e4m3_f32(a.w13[((static_cast<size_t>(e) * 2 + g) * a.I + i) * a.H + k]), d[g]);
-    }
-    for (int g = 0; g < 2; ++g) {
-      for (int o = 16; o > 0; o >>= 1) d[g] += __shfl_xor_sync(0xffffffffu, d[g], o);
-      gu[g] = fmaf(d[g], a.sx[t * a.HB + kb] *
-                             a.s13[((static_cast<size_t>(e) * 2 + g) * a.IB + i / 128) * a.HB + kb], gu[g]);
-    }
-  }
-  if (lane == 0) a.h[static_cast<size_t>(p) * a.I + i] = gu[0] / (1.0f + expf(-gu[0])) * gu[1];
-}
-
-// Codes of h: a CTA of 128 threads per (row, block).
-__global__ void __launch_bounds__(128) moe_quantize_h_kernel(const MoeArgs a) {
-  __shared__ uint32_t mx[4];
-  const int p = blockIdx.x, ib = blockIdx.y, i = ib * 128 + threadIdx.x;
-  const float v = i < a.I ? a.h[static_cast<size_t>(p) * a.I + i] : 0.0f;
-  uint32_t m = abs_bits(v);
-  for (int o = 16; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if ((threadIdx.x & 31) == 0) mx[threadIdx.x >> 5] = m;
   __syncthreads();
-  const float s = fp8_scale(max(max(mx[0], mx[1]), max(mx[2], mx[3])));
-  if (i < a.I) a.hq[static_cast<size_t>(p) * a.I + i] = static_cast<uint8_t>(e4m3x2(__fdiv_rn(v, s), 0.0f));
-  if (threadIdx.x == 0) a.sh[p * a.IB + ib] = s;
+  if (!last) return;
+  __threadfence();
+
+  // this group's logits are complete: a warp per token, E / 32 keys per lane
+  constexpr int kPer = kMoeMaxExperts / 32;
+  const int t = t0 + warp;
+  if (warp < kMoeRouteTokens && t < a.T) {
+    float v[kPer];
+    uint32_t key[kPer];
+    float lmax = 0.0f, mine = 0.0f, chosen = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int x = i * 32 + lane;
+      v[i] = x < a.E ? __ldcg(a.logits + static_cast<size_t>(t) * a.E + x) : 0.0f;
+      key[i] = x < a.E ? moe_key(v[i]) : 0u;
+    }
+    int pick = 0;       // lane j keeps choice j
+    float weight = 0.0f;
+    for (int j = 0; j < a.top; ++j) {
+      uint32_t best = 0;
+      int at = 0;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (key[i] > best) {
+          best = key[i];
+          at = i;
+        }
+      const uint32_t top_key = __reduce_max_sync(0xffffffffu, best);
+      const int e_best = static_cast<int>(__reduce_min_sync(
+          0xffffffffu, best == top_key ? static_cast<uint32_t>(at * 32 + lane) : 0xffffffffu));
+      float lv = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (i * 32 + lane == e_best) {
+          key[i] = 0u;
+          lv = v[i];
+        }
+      lv = __shfl_sync(0xffffffffu, lv, e_best & 31);
+      if (j == 0) lmax = lv;
+      const float ex = expf(lv - lmax);
+      chosen += ex;
+      if (lane == j) {
+        pick = e_best;
+        weight = ex;
+      }
+    }
+    float total = chosen;
+    if (!a.renorm) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (i * 32 + lane < a.E) mine += expf(v[i] - lmax);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+      total = mine;
+    }
+    if (lane < a.top) {
+      a.ids[t * a.top + lane] = pick;
+      a.weights[t * a.top + lane] = weight / total;
+    }
+  }
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    const int ng = (a.T + kMoeRouteTokens - 1) / kMoeRouteTokens;
+    last = atom_add_acq_rel_gpu(&a.cnt->groups, 1u) == static_cast<unsigned>(ng - 1) ? 1 : 0;
+    if (last) a.cnt->groups = 0u;
+  }
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+
+  // every token is routed: the active experts in ascending order, and each
+  // one's weights by token
+  for (int i = threadIdx.x; i < a.E; i += 256) flags[i] = 0u;
+  __syncthreads();
+  const int pairs = a.T * a.top;
+  for (int i = threadIdx.x; i < pairs; i += 256) flags[__ldcg(a.ids + i)] = 1u;
+  __syncthreads();
+  if (warp == 0) {
+    int base = 0;
+    for (int i = 0; i < a.E; i += 32) {
+      const bool on = i + lane < a.E && flags[i + lane] != 0u;
+      const uint32_t m = __ballot_sync(0xffffffffu, on);
+      const int at = base + __popc(m & ((1u << lane) - 1u));
+      if (on && in_bounds(at, a.A)) {
+        slot[i + lane] = at;
+        a.active[1 + at] = i + lane;
+      }
+      base += __popc(m);
+    }
+    if (lane == 0) {
+      a.active[0] = base;
+      last = base;
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < last * a.T; i += 256) a.wt[i] = -1.0f;
+  __syncthreads();
+  for (int i = threadIdx.x; i < pairs; i += 256)
+    a.wt[static_cast<size_t>(slot[__ldcg(a.ids + i)]) * a.T + i / a.top] = __ldcg(a.weights + i);
 }
 
-// y[t, n]: a warp per (token, channel), the choices in order.
-__global__ void __launch_bounds__(256) moe_down_simple_kernel(const MoeArgs a) {
-  const int t = blockIdx.x, lane = threadIdx.x & 31;
-  const int n = blockIdx.y * 8 + (threadIdx.x >> 5);
-  if (n >= a.H) return;
-  float y = 0.0f;
-  for (int j = 0; j < a.top; ++j) {
-    const int p = t * a.top + j, e = a.ids[p];
-    float acc = 0.0f;
-    for (int kb = 0; kb < a.IB; ++kb) {
-      float d = 0.0f;
-      for (int k = kb * 128 + lane; k < min(a.I, kb * 128 + 128); k += 32)
-        d = fmaf(e4m3_f32(a.hq[static_cast<size_t>(p) * a.I + k]),
-                 e4m3_f32(a.w2[(static_cast<size_t>(e) * a.H + n) * a.I + k]), d);
-      for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-      acc = fmaf(d, a.sh[p * a.IB + kb] * a.s2[(static_cast<size_t>(e) * a.HB + n / 128) * a.IB + kb], acc);
+// ------------------------------------------------------------------ experts
+__device__ __forceinline__ unsigned ld_acquire_gpu(const unsigned int* p) {
+  unsigned v;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ void fence_proxy_async_all() {
+  asm volatile("fence.proxy.async;" ::: "memory");
+}
+__device__ __forceinline__ void st_cluster_u32(uint32_t cluster_addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
+}
+
+// Bounded wait until every gate and up CTA has published its part of h.
+__device__ __forceinline__ bool moe_wait_h(const MoeArgs& a, unsigned want) {
+  const long long t0 = clock64();
+  while (ld_acquire_gpu(&a.cnt->h_done) < want) {
+    if (clock64() - t0 > kWaitLimitCycles) {
+      set_dev_error(W4_DEV_ERR_TIMEOUT);
+      return false;
     }
-    y = fmaf(a.weights[p], acc, y);
+    __nanosleep(64);
   }
-  if (lane == 0) a.Y[static_cast<size_t>(t) * a.H + n] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
+  return true;
+}
+
+template <class C>
+__global__ void __launch_bounds__(C::kThreads, C::kMinBlocks)
+    moe_expert_kernel(const __grid_constant__ CUtensorMap xmap,     // xq    {H, T, 1}
+                      const __grid_constant__ CUtensorMap w13map,   // w13   {H, I, 2 E}, 64 rows
+                      const __grid_constant__ CUtensorMap hmap,     // hq    {I, T, A}
+                      const __grid_constant__ CUtensorMap w2map,    // w2    {I, H, E}
+                      const MoeArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* xs = smem;                            // STAGES x kXStage
+  uint8_t* ws = xs + C::STAGES * C::kXStage;     // STAGES x kWStage
+  float* sums = reinterpret_cast<float*>(smem);  // [tokens][kRow], once the ring is idle
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kRing);  // landed (tx)
+  uint64_t* empty = full + C::STAGES;            // MMAs done reading (commit)
+  uint64_t* tfull = empty + C::STAGES;           // block sum ready (commit)   [2]
+  uint64_t* tempty = tfull + 2;                  // block sum read (epilogue)  [2]
+  uint64_t* done = tempty + 2;                   // every MMA complete (commit)
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(done + 1);
+  uint32_t* ticket_slot = tmem_holder + 1;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::STAGES; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&tfull[i], 1);
+      mbar_init(&tempty[i], C::kEpiWarps);
+    }
+    mbar_init(done, 1);
+    fence_barrier_init();
+    grid_dep_launch();
+  }
+  if (warp == C::kMma) {
+    tmem_alloc(tmem_holder, 256);
+    tmem_relinquish();
+  }
+  __syncwarp();
+  cluster_sync();  // every CTA of the cluster runs: its shared memory may be written
+  grid_dep_wait();  // the routing, and the call before it
+  if (threadIdx.x == 0 && rank == 0) {
+    const unsigned t = atomicAdd(&a.cnt->ticket, 1u);
+    for (int r = 0; r < kMoeCluster; ++r) st_cluster_u32(mapa_shared(smem_u32(ticket_slot), r), t);
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  const int ticket = static_cast<int>(*ticket_slot);
+
+  // this CTA's work
+  const int n_active = min(__ldcg(a.active), a.A);
+  const int group = 2 * a.ksplit;                    // CTAs of one 128-channel block of h
+  const int per = kMoeCluster / group;               // such blocks per cluster
+  const int per_expert = (a.IB + per - 1) / per;     // clusters per expert
+  const int up_clusters = n_active * per_expert;
+  const int down_tiles = a.HB;
+  const bool up = ticket < up_clusters;
+  int n = 0;                                         // blocks of K
+  int expert = 0, slot = 0, ib = 0, half64 = 0, k0 = 0, nt = 0;
+  if (up) {
+    slot = ticket / per_expert;
+    expert = __ldcg(a.active + 1 + slot);
+    ib = (ticket - slot * per_expert) * per + rank / group;
+    half64 = rank % group / a.ksplit;
+    const int s = rank % a.ksplit;
+    k0 = a.HB * s / a.ksplit;
+    n = ib < a.IB ? a.HB * (s + 1) / a.ksplit - k0 : 0;
+  } else if (ticket - up_clusters < down_tiles) {
+    nt = ticket - up_clusters;
+    const long long units = static_cast<long long>(n_active) * a.IB;
+    k0 = static_cast<int>(units * rank / kMoeCluster);
+    n = static_cast<int>(units * (rank + 1) / kMoeCluster) - k0;
+  }
+  const bool down = !up && ticket - up_clusters < down_tiles;
+  const unsigned h_want = static_cast<unsigned>(up_clusters) * kMoeCluster;
+  const bool epi = (warp & 3) < C::QUADS && warp < 8;
+
+  if (warp == C::kProducer) {
+    if (lane == 0 && n > 0) {
+      const uint64_t pol_w = policy_evict_first();  // read once
+      const uint64_t pol_x = policy_evict_last();
+      const uint32_t bytes = C::kWStage + static_cast<uint32_t>(a.T) * 128u;
+      auto load_w = [&](int i) {
+        const int s = i % C::STAGES;
+        mbar_arrive_expect_tx(&full[s], bytes);
+        if (up) {
+          const int row = ib * kFp8Block + half64 * 64;
+          tma_load_3d(ws + s * C::kWStage, &w13map, (k0 + i) * 128, row, 2 * expert, &full[s], pol_w);
+          tma_load_3d(ws + s * C::kWStage + 64 * 128, &w13map, (k0 + i) * 128, row, 2 * expert + 1,
+                      &full[s], pol_w);
+        } else {
+          const int act = (k0 + i) / a.IB;
+          tma_load_3d(ws + s * C::kWStage, &w2map, (k0 + i - act * a.IB) * 128, nt * 128,
+                      __ldcg(a.active + 1 + act), &full[s], pol_w);
+        }
+      };
+      auto load_x = [&](int i) {
+        const int s = i % C::STAGES;
+        if (up) {
+          tma_load_3d(xs + s * C::kXStage, &xmap, (k0 + i) * 128, 0, 0, &full[s], pol_x);
+        } else {
+          const int act = (k0 + i) / a.IB;
+          tma_load_3d(xs + s * C::kXStage, &hmap, (k0 + i - act * a.IB) * 128, 0, act, &full[s], pol_x);
+        }
+      };
+      const int early = min(n, C::STAGES);
+      for (int i = 0; i < early; ++i) load_w(i);  // the weights do not wait for h
+      bool ok = up || moe_wait_h(a, h_want);
+      if (!up) fence_proxy_async_all();           // h was written by ordinary stores
+      int i = 0;
+      for (; i < n && (ok || i < early); ++i) {
+        if (i >= C::STAGES) {
+          if (!mbar_wait(&empty[i % C::STAGES], ((i / C::STAGES) - 1) & 1)) break;
+          load_w(i);
+        }
+        load_x(i);  // also after a wait gave up: the armed barriers must complete
+      }
+      // never leave with copies in flight
+      for (int j = i - 1; j >= 0 && j >= i - C::STAGES; --j)
+        mbar_wait(&full[j % C::STAGES], (j / C::STAGES) & 1);
+    }
+  } else if (warp == C::kMma) {
+    constexpr uint32_t idesc = idesc_e4m3_f32(128, 128);
+    const uint64_t xd0 = smem_desc_sw128(smem_u32(xs)), wd0 = smem_desc_sw128(smem_u32(ws));
+    int s = 0;
+    uint32_t phase = 0;
+    for (int i = 0; i < n; ++i) {
+      const int b = i & 1;
+      if (!mbar_wait_warp(&full[s], phase) ||
+          (i >= 2 && !mbar_wait_warp(&tempty[b], ((i >> 1) - 1) & 1)))
+        break;
+      tc_fence_after();
+      const uint64_t xd = xd0 + static_cast<uint32_t>(s) * (C::kXStage >> 4);
+      const uint64_t wd = wd0 + static_cast<uint32_t>(s) * (C::kWStage >> 4);
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          mma_f8_ss(tmem + b * 128, xd + 2 * kk, wd + 2 * kk, idesc, kk > 0 ? 1u : 0u);
+        mma_commit(&empty[s]);
+        mma_commit(&tfull[b]);
+      }
+      __syncwarp();
+      if (++s == C::STAGES) {
+        s = 0;
+        phase ^= 1;
+      }
+    }
+    if (elect_one()) mma_commit(done);
+    __syncwarp();
+  } else if (epi && n > 0) {
+    const int quad = warp & 3, half = warp >> 2;
+    const int row = quad * 32 + lane;
+    const bool busy = quad * 32 < a.T;
+    const int t = min(row, a.T - 1);
+    const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * 64;
+    const uint32_t te0 = smem_u32(&tempty[0]);
+    float acc[64];
+#pragma unroll
+    for (int j = 0; j < 64; ++j) acc[j] = 0.0f;
+    bool ok = true;  // after a wait gave up: go through the motions without waiting
+    if (!up) ok = __all_sync(0xffffffffu, lane != 0 || moe_wait_h(a, h_want));
+    // a block's scale for this token; `on`: the token chose the block's expert
+    bool on = true, on_next = true;
+    auto scale = [&](int i) -> float {
+      if (up) {
+        const int kb = k0 + i;
+        return __ldcg(a.sx + t * a.HB + kb) *
+               __ldg(a.s13 + (static_cast<size_t>(2 * expert + half) * a.IB + ib) * a.HB + kb);
+      }
+      const int act = (k0 + i) / a.IB, kb = k0 + i - act * a.IB;
+      const float w = __ldcg(a.wt + act * a.T + t);
+      on_next = !(w < 0.0f);
+      if (!on_next) return 0.0f;
+      const int e = __ldcg(a.active + 1 + act);
+      return w * (__ldcg(a.sh + (static_cast<size_t>(act) * a.T + t) * a.IB + kb) *
+                  __ldg(a.s2 + (static_cast<size_t>(e) * a.HB + nt) * a.IB + kb));
+    };
+    float f_next = scale(0);
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+      const int b = i & 1;
+      const float f = f_next;
+      on = on_next;
+      f_next = scale(min(i + 1, n - 1));
+      if (ok) ok = mbar_wait_warp(&tfull[b], (i >> 1) & 1);
+      tc_fence_after();
+      if (busy) {
+        uint32_t v[2][16];
+        tmem_ld16(taddr + b * 128, v[0]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          tmem_wait_ld16(v[c & 1]);
+          if (c < 3) tmem_ld16(taddr + b * 128 + 16 * (c + 1), v[(c + 1) & 1]);
+          if (c == 3) {
+            tc_fence_before();
+            __syncwarp();
+            mbar_arrive_lane0(te0 + 8 * b, lane);
+          }
+          // (a lane whose token is not the expert's holds anything: it adds nothing)
+          if (on) {
+#pragma unroll
+            for (int j = 0; j < 16; j += 2)
+              fma2(acc[16 * c + j], acc[16 * c + j + 1], f, v[c & 1][j], v[c & 1][j + 1]);
+          }
+          __syncwarp();
+        }
+      } else {
+        tc_fence_before();
+        mbar_arrive_lane0(te0 + 8 * b, lane);
+      }
+    }
+    // every MMA of this CTA has read its operands, so the ring takes the sums
+    if (ok && row < a.T) {
+      float* dst = sums + row * C::kRow + half * 64;
+#pragma unroll
+      for (int c = 0; c < 16; ++c)
+        *reinterpret_cast<float4*>(dst + 4 * c) =
+            make_float4(acc[4 * c], acc[4 * c + 1], acc[4 * c + 2], acc[4 * c + 3]);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();  // the cluster's sums are in place
+
+  if (up) {
+    // a warp per token: 4 of the block's 128 channels per lane, gate and up
+    // summed over the K ranges in order, h, its largest, its codes
+    const int g0 = rank - rank % group;  // first CTA of this block's group
+    const uint32_t mine = smem_u32(sums);
+    if (ib < a.IB) {
+      for (int t = (rank - g0) * C::kWarps + warp; t < a.T; t += group * C::kWarps) {
+        if (__ldcg(a.wt + slot * a.T + t) < 0.0f) continue;
+        const int owner = g0 + (lane >> 4) * a.ksplit;
+        const uint32_t at = mine + static_cast<uint32_t>(t * C::kRow + (lane & 15) * 4) * 4u;
+        float4 g = make_float4(0.f, 0.f, 0.f, 0.f), u = g;
+        for (int s = 0; s < a.ksplit; ++s) {
+          const float4 gv = ld_cluster_f4(mapa_shared(at, owner + s));
+          const float4 uv = ld_cluster_f4(mapa_shared(at + 256, owner + s));
+          g.x += gv.x; g.y += gv.y; g.z += gv.z; g.w += gv.w;
+          u.x += uv.x; u.y += uv.y; u.z += uv.z; u.w += uv.w;
+        }
+        const float gg[4] = {g.x, g.y, g.z, g.w}, uu[4] = {u.x, u.y, u.z, u.w};
+        float h[4];
+        uint32_t mx = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          h[j] = __fdiv_rn(gg[j], 1.0f + expf(-gg[j])) * uu[j];
+          mx = max(mx, abs_bits(h[j]));
+        }
+        mx = __reduce_max_sync(0xffffffffu, mx);
+        const float sc = fp8_scale(mx);
+        const size_t hrow = static_cast<size_t>(slot) * a.T + t;
+        const int c = ib * kFp8Block + lane * 4;
+        if (c < a.I && in_bounds(hrow * a.I + c + 3, static_cast<unsigned long long>(a.A) * a.T * a.I))
+          *reinterpret_cast<uint32_t*>(a.hq + hrow * a.I + c) =
+              e4m3x2(__fdiv_rn(h[0], sc), __fdiv_rn(h[1], sc)) |
+              (e4m3x2(__fdiv_rn(h[2], sc), __fdiv_rn(h[3], sc)) << 16);
+        if (lane == 0) a.sh[hrow * a.IB + ib] = sc;
+      }
+    }
+    // publish: ordinary stores, read elsewhere by tensor copies and loads
+    fence_proxy_async_all();
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) atom_add_acq_rel_gpu(&a.cnt->h_done, 1u);
+  } else if (down) {
+    const int q0 = 32 * rank / kMoeCluster, w = 32 / kMoeCluster;  // in units of 4 columns
+    const uint32_t mine = smem_u32(sums);
+    const long long units = static_cast<long long>(n_active) * a.IB;
+    for (int e = threadIdx.x; e < a.T * w; e += C::kThreads) {
+      const int r = e / w, c = (q0 + e - r * w) * 4;
+      const uint32_t at = mine + static_cast<uint32_t>(r * C::kRow + c) * 4u;
+      float4 v[kMoeCluster];
+#pragma unroll
+      for (int p = 0; p < kMoeCluster; ++p)  // (an empty K range left no sums)
+        v[p] = units * p / kMoeCluster < units * (p + 1) / kMoeCluster
+                   ? ld_cluster_f4(mapa_shared(at, p))
+                   : make_float4(0.f, 0.f, 0.f, 0.f);
+      float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int p = 0; p < kMoeCluster; ++p) {
+        sum.x += v[p].x;
+        sum.y += v[p].y;
+        sum.z += v[p].z;
+        sum.w += v[p].w;
+      }
+      const int col = nt * 128 + c;
+      uint16_t* y = a.Y + static_cast<size_t>(r) * a.H + col;
+      if (a.vec && col + 4 <= a.H) {
+        *reinterpret_cast<uint2*>(y) = make_uint2(bf16_pack2(sum.x, sum.y), bf16_pack2(sum.z, sum.w));
+      } else {
+        const float s4[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (col + j < a.H) y[j] = __bfloat16_as_ushort(__float2bfloat16_rn(s4[j]));
+      }
+    }
+  }
+  __syncwarp();
+  cluster_sync();  // no CTA leaves while another reads its sums
+  if (threadIdx.x == 0 && rank == 0) {
+    const unsigned clusters = gridDim.x / kMoeCluster;
+    if (atom_add_acq_rel_gpu(&a.cnt->left, 1u) == clusters - 1) {
+      // the last cluster leaves the counters as it found them
+      a.cnt->ticket = 0u;
+      a.cnt->h_done = 0u;
+      a.cnt->left = 0u;
+    }
+  }
+  if (warp == C::kMma) {
+    mbar_wait(done, 0);  // every issued MMA has completed
+    tc_fence_after();
+    tmem_dealloc(tmem, 256);
+  }
 }
 
 }  // namespace w4
