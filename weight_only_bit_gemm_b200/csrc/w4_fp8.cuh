@@ -11,6 +11,11 @@
 // |v| as integers, whose order puts infinity and NaN above every finite value:
 // a block that holds one gets the scale NaN and NaN codes, so a product with
 // it is NaN instead of silently losing the value.
+//
+// The kernels start before the kernel ahead of them on the stream has ended
+// (programmatic dependent launch).  What that kernel may write is read after
+// the dependency wait and from L2 (ld.cg): this SM's L1 can still hold lines
+// that the kernel before it read while this one was already resident.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -92,7 +97,7 @@ __global__ void __launch_bounds__(256) fp8_quantize_x_kernel(const uint16_t* X, 
     const bool have = live && k < K;
     float v[8] = {};
     const size_t at = static_cast<size_t>(m) * K + k;
-    if (have) unpack_bf16x8(*reinterpret_cast<const uint4*>(X + at), v);
+    if (have) unpack_bf16x8(__ldcg(reinterpret_cast<const uint4*>(X + at)), v);
     uint32_t mx = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) mx = max(mx, abs_bits(v[i]));
@@ -175,10 +180,10 @@ __global__ void __launch_bounds__(1024) fp8_add_rmsnorm_kernel(
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[c][j] = 0.0f;
     if (k < K) {
-      unpack_bf16x8(*reinterpret_cast<const uint4*>(x + row + k), v[c]);
+      unpack_bf16x8(__ldcg(reinterpret_cast<const uint4*>(x + row + k)), v[c]);
       if (residual) {
         float r[8];
-        unpack_bf16x8(*reinterpret_cast<const uint4*>(residual + row + k), r);
+        unpack_bf16x8(__ldcg(reinterpret_cast<const uint4*>(residual + row + k)), r);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[c][j] += r[j];
       }

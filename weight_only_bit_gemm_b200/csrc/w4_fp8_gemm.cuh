@@ -355,11 +355,11 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     float4 sx4, sw4;  // of the next group of four
     auto scales = [&](int g) {
       if (a.vec_s) {
-        sx4 = __ldg(reinterpret_cast<const float4*>(sxp + g));
+        sx4 = __ldcg(reinterpret_cast<const float4*>(sxp + g));
         sw4 = __ldg(reinterpret_cast<const float4*>(swp + g));
       } else {
         const int g1 = min(g + 1, a.KB - 1), g2 = min(g + 2, a.KB - 1), g3 = min(g + 3, a.KB - 1);
-        sx4 = make_float4(__ldg(sxp + g), __ldg(sxp + g1), __ldg(sxp + g2), __ldg(sxp + g3));
+        sx4 = make_float4(__ldcg(sxp + g), __ldcg(sxp + g1), __ldcg(sxp + g2), __ldcg(sxp + g3));
         sw4 = make_float4(__ldg(swp + g), __ldg(swp + g1), __ldg(swp + g2), __ldg(swp + g3));
       }
     };
@@ -620,12 +620,36 @@ struct Fp8RowsCfg {
   static_assert(kMinBlocks * (kSmemBytes + 1024) <= 228 * 1024, "shared memory");
 };
 
+// Scales of a thread's blocks in groups of four, requested one group ahead (the
+// loads go to L2, 16 bytes where rows are aligned): f0..f3 are the scales of
+// the current block and the next ones, shifted block by block.
+struct Fp8Scales {
+  float f0, f1, f2, f3;
+  float4 x, w;  // the next group, as loaded
+  __device__ __forceinline__ void load4(const float* px, const float* pw) {
+    x = __ldcg(reinterpret_cast<const float4*>(px));
+    w = __ldg(reinterpret_cast<const float4*>(pw));
+  }
+  __device__ __forceinline__ void take() {
+    f0 = x.x * w.x;
+    f1 = x.y * w.y;
+    f2 = x.z * w.z;
+    f3 = x.w * w.w;
+  }
+  __device__ __forceinline__ void shift() {
+    f0 = f1;
+    f1 = f2;
+    f2 = f3;
+  }
+};
+
 struct Fp8RowsArgs {
   const float* sx;  // [M, KB]
   const float* sw;  // [NB, KB]
   uint16_t* Y;      // bf16 [M, N]
   int M, N, KB;
   int splits;       // CTAs of a cluster: K ranges of a tile
+  int vec_s;        // sx and sw rows are 16-byte aligned
   int vec;          // Y rows are 8-byte aligned
 };
 
@@ -753,15 +777,32 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks)
 #pragma unroll
     for (int j = 0; j < 64; ++j) acc[j] = 0.0f;
     bool ok = true;  // after a wait gave up: go through the motions without waiting
-    float sw_next = __ldg(swp);
+    Fp8Scales sc;
+    // aligned rows: groups of the row's own fours; else from the first block on
+    const int ph = a.vec_s ? k0 & 3 : 0;
+    auto request = [&](int i) {  // the group that starts with block i of this range
+      if (a.vec_s) {
+        sc.load4(sxp + i, swp + i);
+      } else {
+        const int i1 = min(i + 1, n - 1), i2 = min(i + 2, n - 1), i3 = min(i + 3, n - 1);
+        sc.x = make_float4(__ldcg(sxp + i), __ldcg(sxp + i1), __ldcg(sxp + i2), __ldcg(sxp + i3));
+        sc.w = make_float4(__ldg(swp + i), __ldg(swp + i1), __ldg(swp + i2), __ldg(swp + i3));
+      }
+    };
     grid_dep_wait();
-    float sx_next = __ldg(sxp);
+    request(-ph);
+    sc.take();
+    if (4 - ph < n) request(4 - ph);
+    for (int j = 0; j < ph; ++j) sc.shift();
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
-      const int b = i & 1, in = min(i + 1, n - 1);
-      const float f = sx_next * sw_next;
-      sx_next = __ldg(sxp + in);
-      sw_next = __ldg(swp + in);
+      const int b = i & 1;
+      if (i > 0 && ((i + ph) & 3) == 0) {
+        sc.take();
+        if (i + 4 < n) request(i + 4);
+      }
+      const float f = sc.f0;
+      sc.shift();
       if (ok) ok = mbar_wait_warp(&tfull[b], (i >> 1) & 1);
       tc_fence_after();
       if (busy) {

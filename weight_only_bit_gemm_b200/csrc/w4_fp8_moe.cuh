@@ -63,6 +63,7 @@ struct MoeArgs {
   int route_ctas;          // routing CTAs; the ones after them quantize X
   int ksplit;              // K ranges of a gate and up tile
   int vec;                 // Y rows are 8-byte aligned
+  int vec13, vec2;         // rows of s13 and sx, of s2 and sh, are 16-byte aligned
 };
 
 // ------------------------------------------------------------------ routing
@@ -93,7 +94,7 @@ __global__ void __launch_bounds__(256) moe_route_kernel(const MoeArgs a) {
     const bool have = live && k < a.H;
     float v[8] = {};
     const size_t at = static_cast<size_t>(m) * a.H + k;
-    if (have) unpack_bf16x8(*reinterpret_cast<const uint4*>(a.X + at), v);
+    if (have) unpack_bf16x8(__ldcg(reinterpret_cast<const uint4*>(a.X + at)), v);
     uint32_t mx = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) mx = max(mx, abs_bits(v[i]));
@@ -110,17 +111,32 @@ __global__ void __launch_bounds__(256) moe_route_kernel(const MoeArgs a) {
   if (e < a.E) {
     float d[kMoeRouteTokens] = {};
     const uint16_t* r = a.router + static_cast<size_t>(e) * a.H;
-#pragma unroll 4
-    for (int k = lane * 8; k < a.H; k += 256) {
-      float rv[8];
-      unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(r + k)), rv);
+    const int tokens = min(kMoeRouteTokens, a.T - t0);
+    const uint16_t* x = a.X + static_cast<size_t>(t0) * a.H;
+    // 8 chunks of the expert's row in flight, then the tokens' one by one
+    for (int k = lane * 8; k < a.H; k += 8 * 256) {
+      uint4 rw[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        rw[c] = k + c * 256 < a.H ? __ldg(reinterpret_cast<const uint4*>(r + k + c * 256))
+                                  : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
       for (int i = 0; i < kMoeRouteTokens; ++i) {
-        if (t0 + i >= a.T) break;
-        float xv[8];
-        unpack_bf16x8(*reinterpret_cast<const uint4*>(a.X + static_cast<size_t>(t0 + i) * a.H + k), xv);
+        if (i >= tokens) break;
+        uint4 xw[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) d[i] = fmaf(rv[j], xv[j], d[i]);
+        for (int c = 0; c < 8; ++c)
+          xw[c] = k + c * 256 < a.H
+                      ? __ldcg(reinterpret_cast<const uint4*>(x + static_cast<size_t>(i) * a.H + k + c * 256))
+                      : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          float rv[8], xv[8];
+          unpack_bf16x8(rw[c], rv);
+          unpack_bf16x8(xw[c], xv);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) d[i] = fmaf(rv[j], xv[j], d[i]);
+        }
       }
     }
 #pragma unroll
@@ -159,21 +175,25 @@ __global__ void __launch_bounds__(256) moe_route_kernel(const MoeArgs a) {
       uint32_t best = 0;
       int at = 0;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i)
+      for (int i = 0; i < kPer; ++i) {
+        if (i * 32 >= a.E) break;
         if (key[i] > best) {
           best = key[i];
           at = i;
         }
+      }
       const uint32_t top_key = __reduce_max_sync(0xffffffffu, best);
       const int e_best = static_cast<int>(__reduce_min_sync(
           0xffffffffu, best == top_key ? static_cast<uint32_t>(at * 32 + lane) : 0xffffffffu));
       float lv = 0.0f;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i)
+      for (int i = 0; i < kPer; ++i) {
+        if (i * 32 >= a.E) break;
         if (i * 32 + lane == e_best) {
           key[i] = 0u;
           lv = v[i];
         }
+      }
       lv = __shfl_sync(0xffffffffu, lv, e_best & 31);
       if (j == 0) lmax = lv;
       const float ex = expf(lv - lmax);
@@ -186,8 +206,10 @@ __global__ void __launch_bounds__(256) moe_route_kernel(const MoeArgs a) {
     float total = chosen;
     if (!a.renorm) {
 #pragma unroll
-      for (int i = 0; i < kPer; ++i)
+      for (int i = 0; i < kPer; ++i) {
+        if (i * 32 >= a.E) break;
         if (i * 32 + lane < a.E) mine += expf(v[i] - lmax);
+      }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
       total = mine;
@@ -432,29 +454,88 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks)
     for (int j = 0; j < 64; ++j) acc[j] = 0.0f;
     bool ok = true;  // after a wait gave up: go through the motions without waiting
     if (!up) ok = __all_sync(0xffffffffu, lane != 0 || moe_wait_h(a, h_want));
-    // a block's scale for this token; `on`: the token chose the block's expert
-    bool on = true, on_next = true;
-    auto scale = [&](int i) -> float {
-      if (up) {
-        const int kb = k0 + i;
-        return __ldcg(a.sx + t * a.HB + kb) *
-               __ldg(a.s13 + (static_cast<size_t>(2 * expert + half) * a.IB + ib) * a.HB + kb);
-      }
-      const int act = (k0 + i) / a.IB, kb = k0 + i - act * a.IB;
-      const float w = __ldcg(a.wt + act * a.T + t);
-      on_next = !(w < 0.0f);
-      if (!on_next) return 0.0f;
-      const int e = __ldcg(a.active + 1 + act);
-      return w * (__ldcg(a.sh + (static_cast<size_t>(act) * a.T + t) * a.IB + kb) *
-                  __ldg(a.s2 + (static_cast<size_t>(e) * a.HB + nt) * a.IB + kb));
+    // scales, requested a group of four ahead: of the token's codes (or h's) and
+    // of the weights, times (down) the routing weight, whose -1 says that the
+    // token did not choose the block's expert
+    Fp8Scales sc;
+    float w[4], w0 = 1.0f, w1 = 1.0f, w2 = 1.0f, w3 = 1.0f;
+    const int len = up ? a.HB : a.IB;                        // blocks of a row of scales
+    const bool vec = (up ? a.vec13 : a.vec2) != 0;           // rows 16-byte aligned
+    const int ph = vec ? k0 & 3 : 0;
+    int act = up ? 0 : k0 / len, kb = k0 - ph - act * len;   // of the next block to request
+    int left = n + ph;                                       // blocks still to request
+    float wa = 1.0f;
+    const float *pa = nullptr, *pb = nullptr;
+    auto enter = [&]() {  // (down) the expert `act`
+      wa = __ldcg(a.wt + act * a.T + t);
+      pa = a.sh + (static_cast<size_t>(act) * a.T + t) * a.IB;
+      pb = a.s2 + (static_cast<size_t>(__ldcg(a.active + 1 + act)) * a.HB + nt) * a.IB;
     };
-    float f_next = scale(0);
+    if (up) {
+      pa = a.sx + t * a.HB;
+      pb = a.s13 + (static_cast<size_t>(2 * expert + half) * a.IB + ib) * a.HB;
+    } else {
+      enter();
+    }
+    auto request = [&]() {
+      if (left <= 0) return;
+      if (vec) {  // a group never leaves its row
+        if (wa < 0.0f)
+          sc.x = sc.w = make_float4(0.f, 0.f, 0.f, 0.f);  // (h was not written there)
+        else
+          sc.load4(pa + kb, pb + kb);
+        w[0] = w[1] = w[2] = w[3] = wa;
+        left -= 4;
+        kb += 4;
+        if (kb == len && left > 0) {
+          kb = 0;
+          ++act;
+          enter();
+        }
+        return;
+      }
+      float x4[4] = {}, w4[4] = {};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        w[j] = wa;
+        if (left > 0) {
+          --left;
+          x4[j] = wa < 0.0f ? 0.0f : __ldcg(pa + kb);
+          w4[j] = __ldg(pb + kb);
+          if (++kb == len && left > 0) {
+            kb = 0;
+            ++act;
+            enter();
+          }
+        }
+      }
+      sc.x = make_float4(x4[0], x4[1], x4[2], x4[3]);
+      sc.w = make_float4(w4[0], w4[1], w4[2], w4[3]);
+    };
+    auto take = [&]() {
+      sc.take();
+      w0 = w[0];
+      w1 = w[1];
+      w2 = w[2];
+      w3 = w[3];
+      request();
+    };
+    auto shift = [&]() {
+      sc.shift();
+      w0 = w1;
+      w1 = w2;
+      w2 = w3;
+    };
+    request();
+    take();
+    for (int j = 0; j < ph; ++j) shift();
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
       const int b = i & 1;
-      const float f = f_next;
-      on = on_next;
-      f_next = scale(min(i + 1, n - 1));
+      if (i > 0 && ((i + ph) & 3) == 0) take();
+      const bool on = !(w0 < 0.0f);
+      const float f = sc.f0 * w0;
+      shift();
       if (ok) ok = mbar_wait_warp(&tfull[b], (i >> 1) & 1);
       tc_fence_after();
       if (busy) {

@@ -148,6 +148,11 @@ def _stream():
     return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
 
 
+def _raw_stream(dev):
+    """The current stream of device index dev, as an integer."""
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
 def _cuda(t, dtype, name):
     if not (t.is_cuda and t.dtype == dtype and t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor")
@@ -517,86 +522,99 @@ def fp4_gemm(X, Wp, s2, N, K, dq_group=256, out=None, workspace=None):
 # ----------------------------------------------------------------- FP8 (e4m3)
 
 FP8_BLOCK = 128
+_E4M3 = torch.float8_e4m3fn
+_BF16 = torch.bfloat16
+_F32 = torch.float32
+# The decode calls below take a few microseconds on the GPU, so their checks
+# are kept cheap: pointers as plain integers, the stream without a Stream
+# object, one comparison per property.
 
 
 def _blocks(n):
-    return (n + FP8_BLOCK - 1) // FP8_BLOCK
+    return (n + 127) >> 7
 
 
-def _fp8_arg(t, dtype, shape, device, name):
-    """A contiguous tensor of this type, shape and device (None dims: any)."""
-    if t.dtype != dtype or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor on {device}")
-    if t.dim() != len(shape) or any(d is not None and d != n for d, n in zip(shape, t.shape)):
+def _fp8_arg(t, dtype, shape, dev, name):
+    """The address of a contiguous tensor of this type, shape and device."""
+    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor on cuda:{dev}")
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    return t
+    return t.data_ptr()
 
 
-def _fp8_out(out, dtype, shape, device, name):
-    if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    return _fp8_arg(out, dtype, shape, device, name)
-
-
-def _fp8_device(t, name):
-    """The tensor's device, which has to be the current one (the stream is)."""
+def _fp8_first(t, dtype, dim, name):
+    """Device index of a call's first tensor, which has to be the current
+    device (the stream is that device's)."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is "
+    dev = t.get_device()
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{name} is on cuda:{dev}, the current device is "
                          f"cuda:{torch.cuda.current_device()}")
-    return t.device
+    if t.dtype is not dtype or t.dim() != dim or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dim}-dimensional {dtype} tensor")
+    return dev
+
+
+def _fp8_out(out, shape, like, dev):
+    if out is None:
+        return torch.empty(*shape, dtype=_BF16, device=like.device)
+    _fp8_arg(out, _BF16, shape, dev, "out")
+    return out
 
 
 _FP8_WS = {}
 _FP8_COUNTER_BYTES = 65536 * 4
 
 
-def _fp8_workspace(need, workspace, device):
-    """The caller's workspace, or one of this (device, stream), zeroed when it
-    is made.  A call that is being captured into a graph gets its own, zeroed
-    by the graph at each replay: graphs then share none."""
+def _fp8_workspace(need, workspace, like, dev, stream):
+    """(address, bytes) of the caller's workspace, or of one of this (device,
+    stream), zeroed when it is made.  A call that is being captured into a
+    graph gets its own, zeroed by the graph at each replay: graphs then share
+    none."""
     if workspace is not None:
-        _fp8_arg(workspace, torch.uint8, (None,), device, "workspace")
-        return _ws_view(workspace)
-    if torch.cuda.is_current_stream_capturing():
-        buf = torch.empty(need + 256, dtype=torch.uint8, device=device)
+        if workspace.dtype is not torch.uint8 or workspace.get_device() != dev or \
+                not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous torch.uint8 tensor on cuda:{dev}")
+        buf = workspace
+    elif torch.cuda.is_current_stream_capturing():
+        buf = torch.empty(need + 256, dtype=torch.uint8, device=like.device)
         buf[:_FP8_COUNTER_BYTES + 256].zero_()
-        return _ws_view(buf)
-    key = (device.index, torch.cuda.current_stream().cuda_stream)
-    buf = _FP8_WS.get(key)
-    if buf is None or buf.numel() < need + 256:
-        buf = torch.zeros(max(need, 1 << 20) + 256, dtype=torch.uint8, device=device)
-        _FP8_WS[key] = buf
-    return _ws_view(buf)
+    else:
+        buf = _FP8_WS.get((dev, stream))
+        if buf is None or buf.numel() < need + 256:
+            buf = torch.zeros(max(need, 1 << 20) + 256, dtype=torch.uint8, device=like.device)
+            _FP8_WS[dev, stream] = buf
+    at = buf.data_ptr()
+    skip = -at & 255
+    return at + skip, max(0, buf.numel() - skip)
 
 
 def fp8_quantize_weights(W):
     """fp32 W [N, K] or [..., N, K] -> (e4m3 codes of W's shape, fp32 scales
     [..., ceil(N/128), ceil(K/128)]), one scale per 128 x 128 block; K % 16 == 0."""
-    dev = _fp8_device(W, "W")
     if W.dim() < 2:
         raise ValueError("W must have at least two dimensions")
-    _cuda(W, torch.float32, "W")
+    dev = _fp8_first(W, _F32, W.dim(), "W")
     N, K = W.shape[-2:]
     B = W.numel() // (N * K) if N * K > 0 else 0
-    qw = torch.empty(W.shape, dtype=torch.float8_e4m3fn, device=dev)
-    sw = torch.empty(W.shape[:-2] + (_blocks(N), _blocks(K)), dtype=torch.float32, device=dev)
-    _check(lib.fp8_quantize_weights(_ptr(W), B, N, K, _ptr(qw), _ptr(sw), _stream()),
-           "fp8_quantize_weights")
+    qw = torch.empty_like(W, dtype=_E4M3)
+    sw = torch.empty(W.shape[:-2] + (_blocks(N), _blocks(K)), dtype=_F32, device=W.device)
+    _check(lib.fp8_quantize_weights(W.data_ptr(), B, N, K, qw.data_ptr(), sw.data_ptr(),
+                                    _raw_stream(dev)), "fp8_quantize_weights")
     return qw, sw
 
 
 def fp8_quantize_activations(X):
     """bf16 X [M, K] -> (e4m3 codes [M, K], fp32 scales [M, ceil(K/128)]), one
     scale per token and 128 channels; K % 16 == 0."""
-    dev = _fp8_device(X, "X")
-    _fp8_arg(X, torch.bfloat16, (None, None), dev, "X")
+    dev = _fp8_first(X, _BF16, 2, "X")
     M, K = X.shape
-    qx = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=dev)
-    sx = torch.empty((M, _blocks(K)), dtype=torch.float32, device=dev)
-    _check(lib.fp8_quantize_activations(_ptr(X), M, K, _ptr(qx), _ptr(sx), _stream()),
-           "fp8_quantize_activations")
+    qx = torch.empty_like(X, dtype=_E4M3)
+    sx = torch.empty(M, _blocks(K), dtype=_F32, device=X.device)
+    _check(lib.fp8_quantize_activations(X.data_ptr(), M, K, qx.data_ptr(), sx.data_ptr(),
+                                        _raw_stream(dev)), "fp8_quantize_activations")
     return qx, sx
 
 
@@ -605,41 +623,47 @@ def fp8_add_rmsnorm(X, weight, residual=None, eps=1e-6, want_y=False, residual_o
     [M, K] and weight [K]: (codes and scales of y as fp8_quantize_activations
     gives them, bf16 r or None without a residual, bf16 y or None unless
     want_y).  residual_out may be residual (in place)."""
-    dev = _fp8_device(X, "X")
-    _fp8_arg(X, torch.bfloat16, (None, None), dev, "X")
+    dev = _fp8_first(X, _BF16, 2, "X")
     M, K = X.shape
-    _fp8_arg(weight, torch.bfloat16, (K,), dev, "weight")
+    w = _fp8_arg(weight, _BF16, (K,), dev, "weight")
+    device = X.device
+    res = res_out = None
     if residual is not None:
-        _fp8_arg(residual, torch.bfloat16, (M, K), dev, "residual")
-        residual_out = _fp8_out(residual_out, torch.bfloat16, (M, K), dev, "residual_out")
+        res = _fp8_arg(residual, _BF16, X.shape, dev, "residual")
+        if residual_out is None:
+            residual_out = torch.empty_like(X)
+            res_out = residual_out.data_ptr()
+        else:
+            res_out = _fp8_arg(residual_out, _BF16, X.shape, dev, "residual_out")
     elif residual_out is not None:
         raise ValueError("residual_out without a residual")
-    y = torch.empty((M, K), dtype=torch.bfloat16, device=dev) if want_y else None
-    qy = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=dev)
-    sy = torch.empty((M, _blocks(K)), dtype=torch.float32, device=dev)
-    _check(lib.fp8_add_rmsnorm(_ptr(X), _ptr(residual), _ptr(weight), float(eps), M, K,
-                               _ptr(residual_out), _ptr(y), _ptr(qy), _ptr(sy), _stream()),
-           "fp8_add_rmsnorm")
+    y = torch.empty_like(X) if want_y else None
+    qy = torch.empty_like(X, dtype=_E4M3)
+    sy = torch.empty(M, _blocks(K), dtype=_F32, device=device)
+    _check(lib.fp8_add_rmsnorm(X.data_ptr(), res, w, eps, M, K, res_out,
+                               None if y is None else y.data_ptr(), qy.data_ptr(), sy.data_ptr(),
+                               _raw_stream(dev)), "fp8_add_rmsnorm")
     return qy, sy, residual_out, y
 
 
 def fp8_gemm(qx, sx, qw, sw, out=None, workspace=None):
     """bf16 Y[M, N] = (qx sx) . (qw sw)^T for codes and scales as
     fp8_quantize_activations / fp8_add_rmsnorm and fp8_quantize_weights give them."""
-    dev = _fp8_device(qx, "qx")
-    _fp8_arg(qx, torch.float8_e4m3fn, (None, None), dev, "qx")
+    dev = _fp8_first(qx, _E4M3, 2, "qx")
     M, K = qx.shape
-    _fp8_arg(qw, torch.float8_e4m3fn, (None, K), dev, "qw")
     N = qw.shape[0]
-    _fp8_arg(sx, torch.float32, (M, _blocks(K)), dev, "sx")
-    _fp8_arg(sw, torch.float32, (_blocks(N), _blocks(K)), dev, "sw")
-    out = _fp8_out(out, torch.bfloat16, (M, N), dev, "out")
+    w = _fp8_arg(qw, _E4M3, (N, K), dev, "qw")
+    kb = _blocks(K)
+    s1 = _fp8_arg(sx, _F32, (M, kb), dev, "sx")
+    s2 = _fp8_arg(sw, _F32, (_blocks(N), kb), dev, "sw")
+    out = _fp8_out(out, (M, N), qx, dev)
     need = lib.fp8_gemm_workspace_bytes(M, N, K)
     if need == 0:
         raise W4Error(W4_ERR_INVALID_ARG, "fp8_gemm_workspace_bytes")
-    ws = _fp8_workspace(need, workspace, dev)
-    _check(lib.fp8_gemm(_ptr(qx), _ptr(sx), _ptr(qw), _ptr(sw), M, N, K, _ptr(out), _ptr(ws),
-                        ws.numel(), _stream()), "fp8_gemm")
+    stream = _raw_stream(dev)
+    ws, ws_bytes = _fp8_workspace(need, workspace, qx, dev, stream)
+    _check(lib.fp8_gemm(qx.data_ptr(), s1, w, s2, M, N, K, out.data_ptr(), ws, ws_bytes, stream),
+           "fp8_gemm")
     return out
 
 
@@ -648,26 +672,28 @@ def fp8_moe(X, router, w13, s13, w2, s2, top_k, renormalize=True, out=None, work
     router [E, H], gate and up weights w13 [E, 2, I, H] and down weights w2
     [E, H, I] with their scales as fp8_quantize_weights gives them ->
     (bf16 Y [T, H], int32 expert ids [T, top_k], their fp32 weights [T, top_k])."""
-    dev = _fp8_device(X, "X")
-    _fp8_arg(X, torch.bfloat16, (None, None), dev, "X")
+    dev = _fp8_first(X, _BF16, 2, "X")
     T, H = X.shape
-    _fp8_arg(router, torch.bfloat16, (None, H), dev, "router")
-    E = router.shape[0]
-    _fp8_arg(w13, torch.float8_e4m3fn, (E, 2, None, H), dev, "w13")
-    I = w13.shape[2]
-    _fp8_arg(s13, torch.float32, (E, 2, _blocks(I), _blocks(H)), dev, "s13")
-    _fp8_arg(w2, torch.float8_e4m3fn, (E, H, I), dev, "w2")
-    _fp8_arg(s2, torch.float32, (E, _blocks(H), _blocks(I)), dev, "s2")
-    out = _fp8_out(out, torch.bfloat16, (T, H), dev, "out")
+    if w13.dim() != 4:
+        raise ValueError("w13 must have shape (E, 2, I, H)")
+    E, _, I, _ = w13.shape
+    hb, ib = _blocks(H), _blocks(I)
+    r = _fp8_arg(router, _BF16, (E, H), dev, "router")
+    p13 = _fp8_arg(w13, _E4M3, (E, 2, I, H), dev, "w13")
+    q13 = _fp8_arg(s13, _F32, (E, 2, ib, hb), dev, "s13")
+    p2 = _fp8_arg(w2, _E4M3, (E, H, I), dev, "w2")
+    q2 = _fp8_arg(s2, _F32, (E, hb, ib), dev, "s2")
     need = lib.fp8_moe_workspace_bytes(T, E, top_k, H, I)
     if need == 0:
         supported = T <= 128 and E <= 512 and top_k <= 16
         raise W4Error(W4_ERR_INVALID_ARG if supported else W4_ERR_UNSUPPORTED,
                       "fp8_moe_workspace_bytes")
-    ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
-    weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
-    ws = _fp8_workspace(need, workspace, dev)
-    _check(lib.fp8_moe(_ptr(X), _ptr(router), _ptr(w13), _ptr(s13), _ptr(w2), _ptr(s2), T, E,
-                       top_k, H, I, int(bool(renormalize)), _ptr(out), _ptr(ids), _ptr(weights),
-                       _ptr(ws), ws.numel(), _stream()), "fp8_moe")
+    out = _fp8_out(out, (T, H), X, dev)
+    ids = torch.empty(T, top_k, dtype=torch.int32, device=X.device)
+    weights = torch.empty(T, top_k, dtype=_F32, device=X.device)
+    stream = _raw_stream(dev)
+    ws, ws_bytes = _fp8_workspace(need, workspace, X, dev, stream)
+    _check(lib.fp8_moe(X.data_ptr(), r, p13, q13, p2, q2, T, E, top_k, H, I,
+                       1 if renormalize else 0, out.data_ptr(), ids.data_ptr(),
+                       weights.data_ptr(), ws, ws_bytes, stream), "fp8_moe")
     return out, ids, weights
