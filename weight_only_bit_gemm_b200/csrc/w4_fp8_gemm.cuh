@@ -494,10 +494,11 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                 make_float4(acc[4 * c], acc[4 * c + 1], acc[4 * c + 2], acc[4 * c + 3]);
         }
       }
-      __threadfence();
       epi_sync();
       if (threadIdx.x == 128) {
         unsigned int* ctr = a.counter + tt * C::kCtas + static_cast<int>(rank);
+        // (the barrier and this acquire-release publish the CTA's sums and make
+        // the other runs' visible)
         const unsigned prev = atom_add_acq_rel_gpu(ctr, 1u);
         const bool is_last = prev == static_cast<unsigned>(last - first);
         if (is_last) *ctr = 0u;  // leave the workspace zeroed
@@ -505,7 +506,6 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       }
       epi_sync();
       if (*last_flag) {
-        __threadfence();
         constexpr int kQ = C::NT / 4;
         const size_t s0 = slot_of(first);
         const size_t cstep = 2 * static_cast<size_t>(C::kCtas) * a.rows * C::NT;

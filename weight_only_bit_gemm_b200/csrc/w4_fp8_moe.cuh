@@ -146,15 +146,17 @@ __global__ void __launch_bounds__(256) moe_route_kernel(const MoeArgs a) {
       if (lane == 0 && t0 + i < a.T) a.logits[static_cast<size_t>(t0 + i) * a.E + e] = d[i];
     }
   }
-  __threadfence();
+  // (the barrier and thread 0's acquire-release publish the CTA's logits and
+  // make the other CTAs' visible)
   __syncthreads();
   if (threadIdx.x == 0) {
-    last = atom_add_acq_rel_gpu(&a.cnt->group[tg], 1u) == static_cast<unsigned>(eg - 1) ? 1 : 0;
-    if (last) a.cnt->group[tg] = 0u;
+    last = eg == 1 ||
+                   atom_add_acq_rel_gpu(&a.cnt->group[tg], 1u) == static_cast<unsigned>(eg - 1)
+               ? 1 : 0;
+    if (last && eg > 1) a.cnt->group[tg] = 0u;
   }
   __syncthreads();
   if (!last) return;
-  __threadfence();
 
   // this group's logits are complete: a warp per token, E / 32 keys per lane
   constexpr int kPer = kMoeMaxExperts / 32;
@@ -219,16 +221,16 @@ __global__ void __launch_bounds__(256) moe_route_kernel(const MoeArgs a) {
       a.weights[t * a.top + lane] = weight / total;
     }
   }
-  __threadfence();
   __syncthreads();
-  if (threadIdx.x == 0) {
-    const int ng = (a.T + kMoeRouteTokens - 1) / kMoeRouteTokens;
-    last = atom_add_acq_rel_gpu(&a.cnt->groups, 1u) == static_cast<unsigned>(ng - 1) ? 1 : 0;
-    if (last) a.cnt->groups = 0u;
+  const int ng = (a.T + kMoeRouteTokens - 1) / kMoeRouteTokens;
+  if (ng > 1) {
+    if (threadIdx.x == 0) {
+      last = atom_add_acq_rel_gpu(&a.cnt->groups, 1u) == static_cast<unsigned>(ng - 1) ? 1 : 0;
+      if (last) a.cnt->groups = 0u;
+    }
+    __syncthreads();
+    if (!last) return;
   }
-  __syncthreads();
-  if (!last) return;
-  __threadfence();
 
   // every token is routed: the active experts in ascending order, and each
   // one's weights by token
@@ -614,7 +616,6 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks)
     }
     // publish: ordinary stores, read elsewhere by tensor copies and loads
     fence_proxy_async_all();
-    __threadfence();
     __syncthreads();
     if (threadIdx.x == 0) atom_add_acq_rel_gpu(&a.cnt->h_done, 1u);
   } else if (down) {
