@@ -806,21 +806,16 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks)
       if (ok) ok = mbar_wait_warp(&tfull[b], (i >> 1) & 1);
       tc_fence_after();
       if (busy) {
-        uint32_t v[2][16];
-        tmem_ld16(taddr + b * 128, v[0]);
+        // the buffer goes back as soon as its columns are in registers: the
+        // round trip from MMA to MMA bounds a CTA's rate
+        uint32_t v0[32], v1[32];
+        tmem_ld64_wait(taddr + b * 128, v0, v1);
+        tc_fence_before();
+        mbar_arrive_lane0(te0 + 8 * b, lane);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          tmem_wait_ld16(v[c & 1]);
-          if (c < 3) tmem_ld16(taddr + b * 128 + 16 * (c + 1), v[(c + 1) & 1]);
-          if (c == 3) {
-            tc_fence_before();
-            __syncwarp();
-            mbar_arrive_lane0(te0 + 8 * b, lane);
-          }
+        for (int j = 0; j < 32; j += 2) fma2(acc[j], acc[j + 1], f, v0[j], v0[j + 1]);
 #pragma unroll
-          for (int j = 0; j < 16; j += 2)
-            fma2(acc[16 * c + j], acc[16 * c + j + 1], f, v[c & 1][j], v[c & 1][j + 1]);
-        }
+        for (int j = 0; j < 32; j += 2) fma2(acc[32 + j], acc[33 + j], f, v1[j], v1[j + 1]);
       } else {
         tc_fence_before();
         mbar_arrive_lane0(te0 + 8 * b, lane);

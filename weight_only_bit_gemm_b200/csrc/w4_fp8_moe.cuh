@@ -289,6 +289,123 @@ __device__ __forceinline__ bool moe_wait_h(const MoeArgs& a, unsigned want) {
   return true;
 }
 
+// What an epilogue warp needs for a CTA's run of blocks.
+struct MoeBlocks {
+  uint32_t tmem;         // two accumulator buffers of 128 columns
+  uint64_t* tfull;
+  uint32_t tempty;       // shared address
+  float* sums;
+  int n;                 // blocks
+  int k0, act;           // the first one: block of its row of scales, (down) active expert
+  int nt;                // (down) tile of 128 rows
+  const float *pa, *pb;  // (up) scales of the tokens' codes and of the weights' row of blocks
+};
+
+// acc += scale * block sum over the run, for one token (lane) and 64 columns
+// per thread; then the sums go to shared memory.  Scales come in groups of at
+// most four blocks of one row, requested a group ahead (16-byte loads where
+// the rows are aligned).  Down: the scale of h times that of the weights times
+// the routing weight; a token that did not choose the block's expert has the
+// weight -1, h has no row for it, and its lane adds nothing.
+template <bool UP, int ROW>
+__device__ __forceinline__ void moe_block_sums(const MoeArgs& a, const MoeBlocks& q, int warp, int lane) {
+  const int quad = warp & 3, half = warp >> 2;
+  const int row = quad * 32 + lane;
+  const bool busy = quad * 32 < a.T;
+  const int t = min(row, a.T - 1);
+  const uint32_t taddr = q.tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * 64;
+  const int len = UP ? a.HB : a.IB;
+  const bool vec = (UP ? a.vec13 : a.vec2) != 0;
+  const float* pa = UP ? q.pa + t * a.HB : nullptr;
+  const float* pb = q.pb;
+  int act = q.act, kb = q.k0, left = q.n;  // of the next group to request
+  float w_next = 1.0f;
+  auto enter = [&]() {
+    w_next = __ldcg(a.wt + act * a.T + t);
+    pa = a.sh + (static_cast<size_t>(act) * a.T + t) * a.IB;
+    pb = a.s2 + (static_cast<size_t>(__ldcg(a.active + 1 + act)) * a.HB + q.nt) * a.IB;
+  };
+  if (!UP) enter();
+  Fp8Scales sc;
+  float w = 1.0f, w_req = 1.0f;    // of the current group, of the requested one
+  int have = 0, skip_req = 0, have_req = 0;
+  auto request = [&]() {
+    have_req = 0;
+    if (left <= 0) return;
+    if (!UP && kb == len) {
+      kb = 0;
+      ++act;
+      enter();
+    }
+    w_req = w_next;
+    skip_req = vec ? kb & 3 : 0;
+    have_req = min(min(4 - skip_req, len - kb), left);
+    if (!UP && w_next < 0.0f) {
+      sc.x = sc.w = make_float4(0.f, 0.f, 0.f, 0.f);
+    } else if (vec) {
+      sc.load4(pa + (kb & ~3), pb + (kb & ~3));
+    } else {
+      const int k1 = min(kb + 1, len - 1), k2 = min(kb + 2, len - 1), k3 = min(kb + 3, len - 1);
+      sc.x = make_float4(__ldcg(pa + kb), __ldcg(pa + k1), __ldcg(pa + k2), __ldcg(pa + k3));
+      sc.w = make_float4(__ldg(pb + kb), __ldg(pb + k1), __ldg(pb + k2), __ldg(pb + k3));
+    }
+    kb += have_req;
+    left -= have_req;
+  };
+  float acc[64];
+#pragma unroll
+  for (int j = 0; j < 64; ++j) acc[j] = 0.0f;
+  bool ok = true;  // after a wait gave up: go through the motions without waiting
+  request();
+#pragma unroll 1
+  for (int i = 0; i < q.n; ++i) {
+    const int b = i & 1;
+    if (have == 0) {
+      sc.take();
+      for (int j = 0; j < skip_req; ++j) sc.shift();
+      have = have_req;
+      w = w_req;
+      request();
+    }
+    const bool on = UP || !(w < 0.0f);
+    const float f = UP ? sc.f0 : sc.f0 * w;
+    sc.shift();
+    --have;
+    if (ok) ok = mbar_wait_warp(&q.tfull[b], (i >> 1) & 1);
+    tc_fence_after();
+    if (busy) {
+      uint32_t v[2][16];
+      tmem_ld16(taddr + b * 128, v[0]);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        tmem_wait_ld16(v[c & 1]);
+        if (c < 3) tmem_ld16(taddr + b * 128 + 16 * (c + 1), v[(c + 1) & 1]);
+        if (c == 3) {
+          tc_fence_before();
+          mbar_arrive_lane0(q.tempty + 8 * b, lane);
+        }
+        if (on) {
+#pragma unroll
+          for (int j = 0; j < 16; j += 2)
+            fma2(acc[16 * c + j], acc[16 * c + j + 1], f, v[c & 1][j], v[c & 1][j + 1]);
+        }
+        if (!UP) __syncwarp();
+      }
+    } else {
+      tc_fence_before();
+      mbar_arrive_lane0(q.tempty + 8 * b, lane);
+    }
+  }
+  // every MMA of this CTA has read its operands, so the ring takes the sums
+  if (ok && row < a.T) {
+    float* dst = q.sums + row * ROW + half * 64;
+#pragma unroll
+    for (int c = 0; c < 16; ++c)
+      *reinterpret_cast<float4*>(dst + 4 * c) =
+          make_float4(acc[4 * c], acc[4 * c + 1], acc[4 * c + 2], acc[4 * c + 3]);
+  }
+}
+
 template <class C>
 __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks)
     moe_expert_kernel(const __grid_constant__ CUtensorMap xmap,     // xq    {H, T, 1}
@@ -445,133 +562,29 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks)
     if (elect_one()) mma_commit(done);
     __syncwarp();
   } else if (epi && n > 0) {
-    const int quad = warp & 3, half = warp >> 2;
-    const int row = quad * 32 + lane;
-    const bool busy = quad * 32 < a.T;
-    const int t = min(row, a.T - 1);
-    const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * 64;
-    const uint32_t te0 = smem_u32(&tempty[0]);
-    float acc[64];
-#pragma unroll
-    for (int j = 0; j < 64; ++j) acc[j] = 0.0f;
-    bool ok = true;  // after a wait gave up: go through the motions without waiting
-    if (!up) ok = __all_sync(0xffffffffu, lane != 0 || moe_wait_h(a, h_want));
-    // scales, requested a group of four ahead: of the token's codes (or h's) and
-    // of the weights, times (down) the routing weight, whose -1 says that the
-    // token did not choose the block's expert
-    Fp8Scales sc;
-    float w[4], w0 = 1.0f, w1 = 1.0f, w2 = 1.0f, w3 = 1.0f;
-    const int len = up ? a.HB : a.IB;                        // blocks of a row of scales
-    const bool vec = (up ? a.vec13 : a.vec2) != 0;           // rows 16-byte aligned
-    const int ph = vec ? k0 & 3 : 0;
-    int act = up ? 0 : k0 / len, kb = k0 - ph - act * len;   // of the next block to request
-    int left = n + ph;                                       // blocks still to request
-    float wa = 1.0f;
-    const float *pa = nullptr, *pb = nullptr;
-    auto enter = [&]() {  // (down) the expert `act`
-      wa = __ldcg(a.wt + act * a.T + t);
-      pa = a.sh + (static_cast<size_t>(act) * a.T + t) * a.IB;
-      pb = a.s2 + (static_cast<size_t>(__ldcg(a.active + 1 + act)) * a.HB + nt) * a.IB;
-    };
+    MoeBlocks q{};
+    q.tmem = tmem;
+    q.tfull = tfull;
+    q.tempty = smem_u32(&tempty[0]);
+    q.sums = sums;
+    q.n = n;
     if (up) {
-      pa = a.sx + t * a.HB;
-      pb = a.s13 + (static_cast<size_t>(2 * expert + half) * a.IB + ib) * a.HB;
+      const int half = warp >> 2;
+      q.k0 = k0;
+      q.pa = a.sx;
+      q.pb = a.s13 + (static_cast<size_t>(2 * expert + half) * a.IB + ib) * a.HB;
+      moe_block_sums<true, C::kRow>(a, q, warp, lane);
+    } else if (__all_sync(0xffffffffu, lane != 0 || moe_wait_h(a, h_want))) {
+      q.act = k0 / a.IB;
+      q.k0 = k0 - q.act * a.IB;
+      q.nt = nt;
+      moe_block_sums<false, C::kRow>(a, q, warp, lane);
     } else {
-      enter();
-    }
-    auto request = [&]() {
-      if (left <= 0) return;
-      if (vec) {  // a group never leaves its row
-        if (wa < 0.0f)
-          sc.x = sc.w = make_float4(0.f, 0.f, 0.f, 0.f);  // (h was not written there)
-        else
-          sc.load4(pa + kb, pb + kb);
-        w[0] = w[1] = w[2] = w[3] = wa;
-        left -= 4;
-        kb += 4;
-        if (kb == len && left > 0) {
-          kb = 0;
-          ++act;
-          enter();
-        }
-        return;
+      // h never came: let the MMA warp go on without reading its sums
+      for (int i = 0; i < n; ++i) {
+        if (!mbar_wait_warp(&tfull[i & 1], (i >> 1) & 1)) break;
+        mbar_arrive_lane0(smem_u32(&tempty[0]) + 8 * (i & 1), lane);
       }
-      float x4[4] = {}, w4[4] = {};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        w[j] = wa;
-        if (left > 0) {
-          --left;
-          x4[j] = wa < 0.0f ? 0.0f : __ldcg(pa + kb);
-          w4[j] = __ldg(pb + kb);
-          if (++kb == len && left > 0) {
-            kb = 0;
-            ++act;
-            enter();
-          }
-        }
-      }
-      sc.x = make_float4(x4[0], x4[1], x4[2], x4[3]);
-      sc.w = make_float4(w4[0], w4[1], w4[2], w4[3]);
-    };
-    auto take = [&]() {
-      sc.take();
-      w0 = w[0];
-      w1 = w[1];
-      w2 = w[2];
-      w3 = w[3];
-      request();
-    };
-    auto shift = [&]() {
-      sc.shift();
-      w0 = w1;
-      w1 = w2;
-      w2 = w3;
-    };
-    request();
-    take();
-    for (int j = 0; j < ph; ++j) shift();
-#pragma unroll 1
-    for (int i = 0; i < n; ++i) {
-      const int b = i & 1;
-      if (i > 0 && ((i + ph) & 3) == 0) take();
-      const bool on = !(w0 < 0.0f);
-      const float f = sc.f0 * w0;
-      shift();
-      if (ok) ok = mbar_wait_warp(&tfull[b], (i >> 1) & 1);
-      tc_fence_after();
-      if (busy) {
-        uint32_t v[2][16];
-        tmem_ld16(taddr + b * 128, v[0]);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          tmem_wait_ld16(v[c & 1]);
-          if (c < 3) tmem_ld16(taddr + b * 128 + 16 * (c + 1), v[(c + 1) & 1]);
-          if (c == 3) {
-            tc_fence_before();
-            __syncwarp();
-            mbar_arrive_lane0(te0 + 8 * b, lane);
-          }
-          // (a lane whose token is not the expert's holds anything: it adds nothing)
-          if (on) {
-#pragma unroll
-            for (int j = 0; j < 16; j += 2)
-              fma2(acc[16 * c + j], acc[16 * c + j + 1], f, v[c & 1][j], v[c & 1][j + 1]);
-          }
-          __syncwarp();
-        }
-      } else {
-        tc_fence_before();
-        mbar_arrive_lane0(te0 + 8 * b, lane);
-      }
-    }
-    // every MMA of this CTA has read its operands, so the ring takes the sums
-    if (ok && row < a.T) {
-      float* dst = sums + row * C::kRow + half * 64;
-#pragma unroll
-      for (int c = 0; c < 16; ++c)
-        *reinterpret_cast<float4*>(dst + 4 * c) =
-            make_float4(acc[4 * c], acc[4 * c + 1], acc[4 * c + 2], acc[4 * c + 3]);
     }
   }
   __syncwarp();

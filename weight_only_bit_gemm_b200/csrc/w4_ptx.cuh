@@ -457,6 +457,23 @@ __device__ __forceinline__ void tmem_wait_ld16(uint32_t (&v)[16]) {
                  "+r"(v[13]), "+r"(v[14]), "+r"(v[15])::"memory");
 }
 
+// 64 consecutive columns, complete on return.
+__device__ __forceinline__ void tmem_ld64_wait(uint32_t taddr, uint32_t (&a)[32], uint32_t (&b)[32]) {
+  tmem_ld32(taddr, a);
+  tmem_ld32(taddr + 32, b);
+  // the registers are operands of the waits, so that no use of them can be
+  // scheduled above
+#define W4_ALL32(v)                                                                              \
+  "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), \
+      "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]),    \
+      "+r"(v[15]), "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]),  \
+      "+r"(v[22]), "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]),  \
+      "+r"(v[29]), "+r"(v[30]), "+r"(v[31])
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : W4_ALL32(a)::"memory");
+  asm volatile("" : W4_ALL32(b)::"memory");
+#undef W4_ALL32
+}
+
 // True in one lane of a converged warp.  tcgen05.mma takes its descriptors from
 // uniform registers: issued under this predicate, with the operands computed
 // by the whole warp, they are there already; in a branch on the lane number
