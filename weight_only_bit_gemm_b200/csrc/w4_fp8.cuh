@@ -55,15 +55,33 @@ __device__ __forceinline__ void unpack_bf16x8(uint4 w, float (&v)[8]) {
   }
 }
 
-// Codes of 8 values: two words.
+// v / s rounded to nearest for a divisor shared by many values, r = 1 / s
+// rounded to nearest (Markstein, "Computation of elementary functions on the
+// IBM RISC System/6000 processor", 1990: with such an r, and q within one ulp
+// of the quotient, q + r (v - q s) in two fused operations is the correctly
+// rounded quotient).  v r alone can be 1.5 ulp off, so the first step brings q
+// within one ulp and the second rounds correctly.  Needs a normal r and no
+// harmful underflow in v - q s: s >= 1e-25, and then a value so small that its
+// remainder is inexact has the code 0 in any case.
+__device__ __forceinline__ float div_by(float v, float s, float r) {  // s > 0
+  const float q0 = v * r;
+  const float q1 = fmaf(fmaf(-q0, s, v), r, q0);
+  return copysignf(fmaf(fmaf(-q1, s, v), r, q1), v);  // (a zero keeps its sign)
+}
+
+// Codes of 8 values: two words.  (An IEEE division per value costs more
+// instructions than HBM speed leaves, about 16 per value at 3 bytes.)
 __device__ __forceinline__ uint2 fp8_codes8(const float (&v)[8], float s) {
-  float q[8];
+  uint32_t c[4];
+  if (s >= 1e-25f) {
+    const float r = __frcp_rn(s);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(v[i], s);
-  uint2 o;
-  o.x = e4m3x2(q[0], q[1]) | (e4m3x2(q[2], q[3]) << 16);
-  o.y = e4m3x2(q[4], q[5]) | (e4m3x2(q[6], q[7]) << 16);
-  return o;
+    for (int i = 0; i < 4; ++i) c[i] = e4m3x2(div_by(v[2 * i], s, r), div_by(v[2 * i + 1], s, r));
+  } else {  // tiny, or NaN
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = e4m3x2(__fdiv_rn(v[2 * i], s), __fdiv_rn(v[2 * i + 1], s));
+  }
+  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
 // Largest |v| bits over the 16 lanes of this half warp.
@@ -75,35 +93,48 @@ __device__ __forceinline__ uint32_t half_warp_max(uint32_t a) {
 
 // ------------------------------------------------------------- activations
 // Half a warp per (token, 128 channels): 8 channels per lane, one 16-byte
-// load and one 8-byte store.  K % 16 == 0; lanes past K in a row's last block
-// hold nothing.
-__global__ void __launch_bounds__(256) fp8_quantize_x_kernel(const uint16_t* X, int M, int K,
-                                                             FastDivIdx by_kb, uint8_t* q,
+// load and one 8-byte store, U blocks in flight.  K % 16 == 0; with RAGGED the
+// last block of a row is shorter (lanes past K hold nothing), without it the
+// blocks are simply consecutive.
+template <int U, bool RAGGED>
+__global__ void __launch_bounds__(256) fp8_quantize_x_kernel(const uint16_t* X, long long blocks,
+                                                             int K, FastDivIdx by_kb, uint8_t* q,
                                                              float* s) {
   grid_dep_launch();
   grid_dep_wait();
-  const int kb_n = (K + kFp8Block - 1) / kFp8Block;
-  const long long blocks = static_cast<long long>(M) * kb_n;
   const int l = threadIdx.x & 15;
-  const long long step = static_cast<long long>(gridDim.x) * (blockDim.x / 16);
+  const long long step = static_cast<long long>(gridDim.x) * 16;
   // every lane of a warp runs the same number of turns (the shuffles below)
-  const long long first = static_cast<long long>(blockIdx.x) * (blockDim.x / 16);
-  for (long long b0 = first; b0 < blocks; b0 += step) {
-    const long long b = b0 + threadIdx.x / 16;
-    const bool live = b < blocks;
-    const long long m = live ? static_cast<long long>(fast_div(static_cast<unsigned long long>(b), by_kb)) : 0;
-    const int kb = live ? static_cast<int>(b - m * kb_n) : 0;
-    const int k = kb * kFp8Block + l * 8;
-    const bool have = live && k < K;
-    float v[8] = {};
-    const size_t at = static_cast<size_t>(m) * K + k;
-    if (have) unpack_bf16x8(__ldcg(reinterpret_cast<const uint4*>(X + at)), v);
-    uint32_t mx = 0;
+  for (long long b0 = static_cast<long long>(blockIdx.x) * 16; b0 < blocks; b0 += U * step) {
+    uint4 w[U];
+    size_t at[U];
+    bool have[U];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) mx = max(mx, abs_bits(v[i]));
-    const float sc = fp8_scale(half_warp_max(mx));
-    if (have) *reinterpret_cast<uint2*>(q + at) = fp8_codes8(v, sc);
-    if (live && l == 0) s[b] = sc;
+    for (int u = 0; u < U; ++u) {
+      const long long b = b0 + u * step + threadIdx.x / 16;
+      have[u] = b < blocks;
+      at[u] = static_cast<size_t>(b) * kFp8Block + l * 8;
+      if (RAGGED) {
+        const int kb_n = (K + kFp8Block - 1) / kFp8Block;
+        const unsigned long long m = have[u] ? fast_div(static_cast<unsigned long long>(b), by_kb) : 0;
+        const int k = static_cast<int>(b - static_cast<long long>(m) * kb_n) * kFp8Block + l * 8;
+        have[u] = have[u] && k < K;
+        at[u] = static_cast<size_t>(m) * K + k;
+      }
+      w[u] = have[u] ? __ldcg(reinterpret_cast<const uint4*>(X + at[u])) : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float v[8];
+      unpack_bf16x8(w[u], v);
+      uint32_t mx = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) mx = max(mx, abs_bits(v[i]));
+      const float sc = fp8_scale(half_warp_max(mx));
+      if (have[u]) *reinterpret_cast<uint2*>(q + at[u]) = fp8_codes8(v, sc);
+      const long long b = b0 + u * step + threadIdx.x / 16;
+      if (l == 0 && b < blocks) s[b] = sc;
+    }
   }
 }
 
@@ -111,7 +142,7 @@ __global__ void __launch_bounds__(256) fp8_quantize_x_kernel(const uint16_t* X, 
 // One CTA per 128 x 128 block of one of B matrices: 16 lanes per row, 8
 // channels per lane, 16 rows at a time; the values stay in registers between
 // the maximum and the codes.
-__global__ void __launch_bounds__(256) fp8_quantize_w_kernel(const float* W, int N, int K,
+__global__ void __launch_bounds__(256, 3) fp8_quantize_w_kernel(const float* W, int N, int K,
                                                              uint8_t* q, float* s) {
   __shared__ uint32_t wmax[8];
   const uint32_t kb_n = (K + kFp8Block - 1) / kFp8Block, nb_n = (N + kFp8Block - 1) / kFp8Block;
