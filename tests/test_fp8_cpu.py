@@ -118,19 +118,23 @@ def test_host_tensors_refused(call):
 
 def plan(M, N, K, sms=148):
     """The library's split above 128 tokens (148 SMs is its count without a device)."""
-    p = dict(KB=-(-K // 128), workers=sms // 2, runs=0)
-    tiles = -(-M // 256) * -(-N // 256)
-    p["rounds"], p["tail"] = divmod(tiles, p["workers"])
-    units = p["tail"] * p["KB"]
-    best = p["KB"]
-    for runs in range(p["tail"] + 1, p["workers"] + 1):
-        if p["tail"] == 0 or runs > units:
-            break
-        cost = units / runs + 5 + 128 * 256 * 4 / 44000 * (1 + runs / p["tail"])
-        if cost < best:
-            best, p["runs"] = cost, runs
-    p["partial"] = 2 * p["runs"] * 2 * 128 * 256
-    return p
+    best = None
+    for nt, block, read in ((256, 0.56, 3.0), (128, 0.36, 2.0)):
+        p = dict(KB=-(-K // 128), workers=sms // 2, runs=0)
+        p["rounds"], p["tail"] = divmod(-(-M // 256) * -(-N // nt), p["workers"])
+        units = p["tail"] * p["KB"]
+        cost = p["KB"] * block + 1.5 if p["tail"] else 0.0
+        for runs in range(p["tail"] + 1, p["workers"] + 1):
+            if p["tail"] == 0 or runs > units:
+                break
+            c = units / runs * block + 10 + read * (1 + runs / p["tail"])
+            if c < cost:
+                cost, p["runs"] = c, runs
+        cost += p["rounds"] * (p["KB"] * block + 1.5)
+        p["partial"] = 2 * p["runs"] * 2 * 128 * nt
+        if best is None or cost < best:
+            best, chosen = cost, p
+    return chosen
 
 
 SHAPES = [(M, N, K) for M in (129, 256, 511, 2048, 8192)

@@ -22,8 +22,8 @@
 // distributed shared memory.
 //
 // More tokens (fp8_tc_gemm_kernel): CTA pairs (cta_group::2) of 256 tokens x
-// 256 weight rows, each CTA staging half of each operand, in a persistent
-// grid.  Each worker (CTA or pair) takes whole tiles while
+// 256 or 128 weight rows, each CTA staging half of each operand, in a
+// persistent grid.  Each worker (CTA or pair) takes whole tiles while
 // every worker gets one; the tiles left over are cut along K into equal runs
 // of blocks, one per worker, whose fp32 partial sums the last run of a tile
 // to finish adds in the order of K (the result does not depend on which
@@ -42,28 +42,29 @@ constexpr int kFp8Rows = 128;        // tokens per CTA tile (tensor-memory lanes
 constexpr int kFp8EpiWarps = 8;
 constexpr uint16_t kFp8PairMask = 0x3;
 
-template <int NT_, bool PAIR_, int STAGES_>
+// A CTA pair's tile: 256 tokens x NT weight rows.  NT = 256 moves the fewest
+// operand bytes through L2 per product; NT = 128 leaves smaller tiles, which
+// fill the last wave of a few better.
+template <int NT_, int STAGES_>
 struct Fp8Cfg {
-  static constexpr int NT = NT_;            // weight rows (MMA columns) per tile
-  static constexpr bool PAIR = PAIR_;
+  static constexpr int NT = NT_;             // weight rows (MMA columns) per tile
   static constexpr int STAGES = STAGES_;
-  static constexpr int kCtas = PAIR ? 2 : 1;
-  static constexpr int kWRows = NT / kCtas;  // weight rows this CTA stages
+  static constexpr int kWRows = NT / 2;      // weight rows this CTA stages
   static constexpr int kXStage = kFp8Rows * 128;
   static constexpr int kWStage = kWRows * 128;
   static constexpr int kThreads = 128 + kFp8EpiWarps * 32;
-  // pairs: 128 running sums per epilogue thread; registers move to them from
-  // the first warpgroup: (104 + 2 * 200) * 128 = 168 * 384 threads
-  static constexpr bool kRegSplit = PAIR;
-  static constexpr int kLaunchRegs = 168, kFewRegs = 104, kManyRegs = 200;
+  static constexpr int kCols = NT / 2;       // columns (running sums) per epilogue thread
+  static constexpr int kBufs = 512 / NT;     // block sums in tensor memory, all 512 columns
+  // 128 running sums per thread need registers from the first warpgroup:
+  // (120 + 2 * 192) * 128 = 168 * 384 threads
+  static constexpr bool kRegSplit = NT == 256;
+  static constexpr int kLaunchRegs = 168, kFewRegs = 120, kManyRegs = 192;
   static_assert(kFewRegs * 128 + kManyRegs * 256 <= kLaunchRegs * kThreads, "register shares");
-  static constexpr int kCols = NT / 2;       // columns per epilogue thread
-  static constexpr int kTmemCols = 2 * NT;
   // per epilogue warp, a box of 32 tokens x 64 outputs in bf16 (128-byte rows)
   // in the 128-byte swizzle
   static constexpr int kYWarp = 32 * 64 * 2;
   static constexpr int kSmemBytes = 1024 + STAGES * (kXStage + kWStage) + kFp8EpiWarps * kYWarp +
-                                    (2 * STAGES + 5) * 8 + 16;
+                                    (2 * STAGES + 2 * kBufs + 1) * 8 + 16;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 };
 
@@ -71,7 +72,7 @@ struct Fp8GemmArgs {
   const float* sx;        // [M, KB]
   const float* sw;        // [NB, KB]
   uint16_t* Y;            // bf16 [M, N]
-  float* partial;         // [slot][rows][NT]: two slots per worker (and CTA of a pair)
+  float* partial;         // two slots of 128 tokens x NT per worker and CTA of the pair
   unsigned int* counter;  // [tail tile (and CTA of a pair)], zero between calls
   int M, N, KB, NB;
   int tiles_m, tiles_n, group_m;
@@ -79,7 +80,6 @@ struct Fp8GemmArgs {
   int rounds;             // whole tiles per worker
   int tail;               // tiles left over, the last ones
   int tail_workers;       // runs they are cut into (0: each whole, one worker each)
-  int rows;               // rows of a partial slot
   int vec_s;              // sx and sw rows are 16-byte aligned
   int vec;                // Y rows are 16-byte aligned: tensor copies and vector stores
   int keep_w;             // weights are read by several token tiles: keep them in L2
@@ -95,7 +95,7 @@ struct Fp8Piece {
 struct Fp8Work {
   const Fp8GemmArgs& a;
   int w, round;
-  long long u, end;
+  int u, end;  // (the host cuts a tail only where units * workers fits in 31 bits)
   __device__ __forceinline__ Fp8Work(const Fp8GemmArgs& args, int worker)
       : a(args), w(worker), round(0), u(0), end(0) {
     if (a.tail_workers > 0 && w < a.tail_workers) {
@@ -103,11 +103,11 @@ struct Fp8Work {
       end = run_start(w + 1);
     }
   }
-  __device__ __forceinline__ long long units() const { return static_cast<long long>(a.tail) * a.KB; }
-  __device__ __forceinline__ long long run_start(int c) const { return units() * c / a.tail_workers; }
+  __device__ __forceinline__ int units() const { return a.tail * a.KB; }
+  __device__ __forceinline__ int run_start(int c) const { return units() * c / a.tail_workers; }
   // the worker whose run holds unit v
-  __device__ __forceinline__ int run_of(long long v) const {
-    return static_cast<int>(((v + 1) * a.tail_workers - 1) / units());
+  __device__ __forceinline__ int run_of(int v) const {
+    return ((v + 1) * a.tail_workers - 1) / units();
   }
   __device__ __forceinline__ bool next(Fp8Piece& p) {
     const int whole = a.rounds + (a.tail_workers == 0 && w < a.tail ? 1 : 0);
@@ -119,11 +119,10 @@ struct Fp8Work {
       return true;
     }
     if (u >= end) return false;
-    const int t = static_cast<int>(u / a.KB);
+    const int t = u / a.KB;
     p.tile = a.rounds * a.workers + t;
-    p.k0 = static_cast<int>(u - static_cast<long long>(t) * a.KB);
-    const long long left = end - u;
-    p.k1 = left < a.KB - p.k0 ? p.k0 + static_cast<int>(left) : a.KB;
+    p.k0 = u - t * a.KB;
+    p.k1 = min(a.KB, p.k0 + end - u);
     u += p.k1 - p.k0;
     return true;
   }
@@ -163,43 +162,35 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   uint8_t* ys = ws + C::STAGES * C::kWStage;            // 8 x kYWarp
   uint64_t* full = reinterpret_cast<uint64_t*>(ys + kFp8EpiWarps * C::kYWarp);  // landed (tx)
   uint64_t* empty = full + C::STAGES;                   // MMAs done reading (commit)
-  uint64_t* tfull = empty + C::STAGES;                  // block sum ready (commit)  [2]
-  uint64_t* tempty = tfull + 2;                         // block sum read (8 or 16 warps) [2]
-  uint64_t* done = tempty + 2;                          // every MMA complete (commit)
+  uint64_t* tfull = empty + C::STAGES;                  // block sum ready (commit)       [kBufs]
+  uint64_t* tempty = tfull + C::kBufs;                  // block sum read (both CTAs' warps) [kBufs]
+  uint64_t* done = tempty + C::kBufs;                   // every MMA complete (commit)
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(done + 1);
   int* last_flag = reinterpret_cast<int*>(tmem_holder + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = C::PAIR ? cluster_ctarank() : 0u;
-  const int worker = static_cast<int>(blockIdx.x) / C::kCtas;
+  const uint32_t rank = cluster_ctarank();
+  const int worker = static_cast<int>(blockIdx.x) / 2;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::STAGES; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < C::kBufs; ++i) {
       mbar_init(&tfull[i], 1);
-      mbar_init(&tempty[i], C::kCtas * kFp8EpiWarps);
+      mbar_init(&tempty[i], 2 * kFp8EpiWarps);
     }
     mbar_init(done, 1);
     fence_barrier_init();
     grid_dep_launch();
   }
   if (warp == 1) {
-    if constexpr (C::PAIR) {
-      tmem_alloc_pair(tmem_holder, C::kTmemCols);
-      tmem_relinquish_pair();
-    } else {
-      tmem_alloc(tmem_holder, C::kTmemCols);
-      tmem_relinquish();
-    }
+    tmem_alloc_pair(tmem_holder, 512);
+    tmem_relinquish_pair();
   }
   tc_fence_before();
-  if constexpr (C::PAIR)
-    cluster_sync();  // the peer's copies and arrivals target this CTA's barriers
-  else
-    __syncthreads();
+  cluster_sync();  // the peer's copies and arrivals target this CTA's barriers
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   Fp8Work work(a, worker);
@@ -213,27 +204,19 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       prefetch_tensormap(&xmap);
       const uint64_t pol_w = a.keep_w ? policy_evict_normal() : policy_evict_first();
       const uint64_t pol_x = policy_evict_last();
-      constexpr uint32_t kBytes = C::kCtas * C::kWStage;
-      // the X box may be shorter than the stage's 128 rows; its bytes are counted as copied
-      const uint32_t x_bytes = static_cast<uint32_t>(C::kCtas) * static_cast<uint32_t>(a.rows) * 128u;
+      constexpr uint32_t kBytes = 2 * (C::kXStage + C::kWStage);
       auto arm = [&](int s) {  // a pair: the leader's barrier counts both CTAs' bytes
-        if (rank == 0) mbar_arrive_expect_tx(&full[s], kBytes + x_bytes);
+        if (rank == 0) mbar_arrive_expect_tx(&full[s], kBytes);
       };
       auto load_w = [&](int s, int nt, int kb) {
-        if constexpr (C::PAIR)
-          tma_load_3d_pair(ws + s * C::kWStage, &wmap, kb * 128,
-                           nt * C::NT + static_cast<int>(rank) * C::kWRows, 0,
-                           mapa_shared(smem_u32(&full[s]), 0), pol_w);
-        else
-          tma_load_3d(ws + s * C::kWStage, &wmap, kb * 128, nt * C::NT, 0, &full[s], pol_w);
+        tma_load_3d_pair(ws + s * C::kWStage, &wmap, kb * 128,
+                         nt * C::NT + static_cast<int>(rank) * C::kWRows, 0,
+                         mapa_shared(smem_u32(&full[s]), 0), pol_w);
       };
       auto load_x = [&](int s, int mt, int kb) {
-        const int m = (mt * C::kCtas + static_cast<int>(rank)) * kFp8Rows;
-        if constexpr (C::PAIR)
-          tma_load_3d_pair(xs + s * C::kXStage, &xmap, kb * 128, m, 0,
-                           mapa_shared(smem_u32(&full[s]), 0), pol_x);
-        else
-          tma_load_3d(xs + s * C::kXStage, &xmap, kb * 128, m, 0, &full[s], pol_x);
+        const int m = (mt * 2 + static_cast<int>(rank)) * kFp8Rows;
+        tma_load_3d_pair(xs + s * C::kXStage, &xmap, kb * 128, m, 0,
+                         mapa_shared(smem_u32(&full[s]), 0), pol_x);
       };
       // the weights do not depend on the previous kernel: the first ring of
       // them is requested before the dependency wait
@@ -279,16 +262,17 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     if (rank == 0) {
-      constexpr uint32_t idesc = idesc_e4m3_f32(C::kCtas * 128, C::NT);
+      constexpr uint32_t idesc = idesc_e4m3_f32(2 * 128, C::NT);
       const uint64_t xd0 = smem_desc_sw128(smem_u32(xs)), wd0 = smem_desc_sw128(smem_u32(ws));
-      int s = 0, it = 0;
+      int s = 0;
+      uint32_t it = 0;
       uint32_t phase = 0;
       bool ok = true;
       while (ok && work.next(p)) {
         for (int kb = p.k0; kb < p.k1; ++kb, ++it) {
-          const int b = it & 1;
+          const uint32_t b = it & (C::kBufs - 1);
           ok = mbar_wait_warp(&full[s], phase) &&
-               (it < 2 || mbar_wait_warp(&tempty[b], ((it >> 1) - 1) & 1));
+               (it < C::kBufs || mbar_wait_warp(&tempty[b], ((it / C::kBufs) - 1) & 1));
           if (!ok) break;
           tc_fence_after();
           // descriptor addresses are in units of 16 bytes
@@ -298,18 +282,10 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
-              if constexpr (C::PAIR)
-                mma_f8_ss_pair(d, xd + 2 * kk, wd + 2 * kk, idesc, kk > 0 ? 1u : 0u);
-              else
-                mma_f8_ss(d, xd + 2 * kk, wd + 2 * kk, idesc, kk > 0 ? 1u : 0u);
+              mma_f8_ss_pair(d, xd + 2 * kk, wd + 2 * kk, idesc, kk > 0 ? 1u : 0u);
             }
-            if constexpr (C::PAIR) {
-              mma_commit_pair(&empty[s], kFp8PairMask);
-              mma_commit_pair(&tfull[b], kFp8PairMask);
-            } else {
-              mma_commit(&empty[s]);
-              mma_commit(&tfull[b]);
-            }
+            mma_commit_pair(&empty[s], kFp8PairMask);
+            mma_commit_pair(&tfull[b], kFp8PairMask);
           }
           __syncwarp();
           if (++s == C::STAGES) {
@@ -319,10 +295,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         }
       }
       if (elect_one()) {
-        if constexpr (C::PAIR)
-          mma_commit_pair(done, kFp8PairMask);
-        else
-          mma_commit(done);
+        mma_commit_pair(done, kFp8PairMask);
       }
       __syncwarp();
     }
@@ -335,17 +308,14 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * C::kCols;
     uint8_t* yw = ys + (warp - 4) * C::kYWarp;
     bool ok = true;  // after a wait gave up: go through the motions without waiting
-    int it = 0;
+    uint32_t it = 0;
     // this warp has read accumulator buffer b
     // (a pair: on the leader's barrier)
-    const uint32_t te0 = C::PAIR ? mapa_shared(smem_u32(&tempty[0]), 0) : smem_u32(&tempty[0]);
-    auto release = [&](int b) {
+    const uint32_t te0 = mapa_shared(smem_u32(&tempty[0]), 0);
+    auto release = [&](uint32_t b) {
       tc_fence_before();
       __syncwarp();
-      if constexpr (C::PAIR)
-        mbar_arrive_cluster_lane0(te0 + 8 * b, lane);
-      else
-        mbar_arrive_lane0(te0 + 8 * b, lane);
+      mbar_arrive_cluster_lane0(te0 + 8 * b, lane);
     };
     // Scales, four blocks at a time and four ahead: a token's are contiguous, so
     // the 32 lanes' loads touch 32 lines, and shared memory and L1 have one data
@@ -365,7 +335,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     };
     auto begin = [&](const Fp8Piece& q) {
       work.tile_at(q.tile, mt, nt);
-      const int m = (mt * C::kCtas + static_cast<int>(rank)) * kFp8Rows + row;
+      const int m = (mt * 2 + static_cast<int>(rank)) * kFp8Rows + row;
       const int nb = (nt * C::NT + half * C::kCols) / kFp8Block;
       sxp = a.sx + static_cast<size_t>(min(m, a.M - 1)) * a.KB;
       swp = a.sw + static_cast<size_t>(min(nb, a.NB - 1)) * a.KB;
@@ -377,7 +347,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     if (have) begin(nx);
     while (have) {
       p = nx;
-      const int m0 = (mt * C::kCtas + static_cast<int>(rank)) * kFp8Rows;
+      const int m0 = (mt * 2 + static_cast<int>(rank)) * kFp8Rows;
       const int rows = min(kFp8Rows, a.M - m0);  // may be <= 0 in a pair's second CTA
       const bool busy = quad * 32 < rows;
       const int ntile = nt, n0 = nt * C::NT + half * C::kCols;
@@ -401,8 +371,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
 #pragma unroll 1
       for (int kb = p.k0; kb < p.k1; ++kb, ++it) {
         const float f = f0;
-        const int b = it & 1;
-        if (ok) ok = mbar_wait_warp(&tfull[b], (it >> 1) & 1);
+        const uint32_t b = it & (C::kBufs - 1);
+        if (ok) ok = mbar_wait_warp(&tfull[b], (it / C::kBufs) & 1);
         tc_fence_after();
         if (busy) {
           // the next 16 columns load while the last are added
@@ -477,26 +447,25 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       // a run of the tail: publish the partial sums; the last run of the tile
       // to arrive adds them in the order of K
       const int tt = p.tile - a.rounds * a.workers;
-      const long long ubase = static_cast<long long>(tt) * a.KB;
+      const int ubase = tt * a.KB;
       const int first = work.run_of(ubase), last = work.run_of(ubase + a.KB - 1);
       // a worker's run starts in this tile, or ends here after the one before
+      constexpr size_t kSlot = static_cast<size_t>(kFp8Rows) * C::NT;
       auto slot_of = [&](int c) -> size_t {
         const size_t idx = work.run_start(c) < ubase ? 1 : 0;
-        return ((static_cast<size_t>(c) * 2 + idx) * C::kCtas + rank) * static_cast<size_t>(a.rows) * C::NT;
+        return ((static_cast<size_t>(c) * 2 + idx) * 2 + rank) * kSlot;
       };
+      // a slot is [4 columns][token]: the lanes of a store are consecutive
       const size_t mine = slot_of(worker);
-      if (row < rows) {
-        float* dst = a.partial + mine + static_cast<size_t>(row) * C::NT + half * C::kCols;
-        if (in_bounds(mine + static_cast<size_t>(row) * C::NT + C::NT - 1, a.partial_floats)) {
+      if (row < rows && in_bounds(mine + kSlot - 1, a.partial_floats)) {
+        float4* dst = reinterpret_cast<float4*>(a.partial + mine) + (half * C::kCols / 4) * kFp8Rows + row;
 #pragma unroll
-          for (int c = 0; c < C::kCols / 4; ++c)
-            *reinterpret_cast<float4*>(dst + 4 * c) =
-                make_float4(acc[4 * c], acc[4 * c + 1], acc[4 * c + 2], acc[4 * c + 3]);
-        }
+        for (int c = 0; c < C::kCols / 4; ++c)
+          dst[c * kFp8Rows] = make_float4(acc[4 * c], acc[4 * c + 1], acc[4 * c + 2], acc[4 * c + 3]);
       }
       epi_sync();
       if (threadIdx.x == 128) {
-        unsigned int* ctr = a.counter + tt * C::kCtas + static_cast<int>(rank);
+        unsigned int* ctr = a.counter + tt * 2 + static_cast<int>(rank);
         // (the barrier and this acquire-release publish the CTA's sums and make
         // the other runs' visible)
         const unsigned prev = atom_add_acq_rel_gpu(ctr, 1u);
@@ -506,70 +475,69 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       }
       epi_sync();
       if (*last_flag) {
-        constexpr int kQ = C::NT / 4;
         const size_t s0 = slot_of(first);
-        const size_t cstep = 2 * static_cast<size_t>(C::kCtas) * a.rows * C::NT;
         // runs after the first start inside this tile: their first slots
-        const size_t s1 = ((static_cast<size_t>(first) * 2) * C::kCtas + rank) *
-                          static_cast<size_t>(a.rows) * C::NT;
-        // loads in flight per L2 round trip: 8 runs of one element (few tokens)
-        // or 2 runs of 4 elements; the additions stay in the order of the runs
+        const size_t s1 = (static_cast<size_t>(first) * 4 + rank) * kSlot;
+        // a thread adds 8 columns of one token, kE such elements of two runs in
+        // flight (16 loads per L2 round trip: the reading is latency-bound); the
+        // additions stay in the order of the runs
+        constexpr int kE = 4, kRuns = 2, kStep = kFp8EpiWarps * 32;
         const int tid = static_cast<int>(threadIdx.x) - 128;
-        const int total = rows * kQ;
-        auto sum_of = [&](auto elems, auto runs, int e0) {
-          constexpr int kE = decltype(elems)::value, kR = decltype(runs)::value;
-          float4 sum[kE];
-#pragma unroll
-          for (int j = 0; j < kE; ++j) sum[j] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-          for (int c = first; c <= last; c += kR) {
-            float4 v[kR][kE];
+        for (int e0 = tid; e0 < kFp8Rows * C::NT / 8; e0 += kE * kStep) {
+          float4 sum[kE][2];
 #pragma unroll
-            for (int u = 0; u < kR; ++u) {
-              const size_t src = c + u == first ? s0 : s1 + (c + u - first) * cstep;
+          for (int j = 0; j < kE; ++j) sum[j][0] = sum[j][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+          for (int c = first; c <= last; c += kRuns) {
+            float4 v[kRuns][kE][2];
+#pragma unroll
+            for (int u = 0; u < kRuns; ++u) {
+              const size_t slot = c + u == first ? s0 : s1 + static_cast<size_t>(c + u - first) * 4 * kSlot;
+              const float4* src = reinterpret_cast<const float4*>(a.partial + slot);
 #pragma unroll
               for (int j = 0; j < kE; ++j) {
-                const int e = e0 + j * kFp8EpiWarps * 32;
-                const size_t at = src + static_cast<size_t>(e) * 4;
-                v[u][j] = c + u <= last && e < total && in_bounds(at + 3, a.partial_floats)
-                              ? __ldcg(reinterpret_cast<const float4*>(a.partial + at))
-                              : make_float4(0.f, 0.f, 0.f, 0.f);
+                const int e = e0 + j * kStep;
+                const int r = e % kFp8Rows, c8 = e / kFp8Rows;
+                const bool live = c + u <= last && r < rows &&
+                                  in_bounds(slot + kSlot - 1, a.partial_floats);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                  v[u][j][h] = live ? __ldcg(src + (2 * c8 + h) * kFp8Rows + r)
+                                    : make_float4(0.f, 0.f, 0.f, 0.f);
               }
             }
 #pragma unroll
-            for (int u = 0; u < kR; ++u)
+            for (int u = 0; u < kRuns; ++u) {
+              if (c + u > last) break;
 #pragma unroll
-              for (int j = 0; j < kE; ++j) {
-                if (c + u > last) continue;
-                sum[j].x += v[u][j].x;
-                sum[j].y += v[u][j].y;
-                sum[j].z += v[u][j].z;
-                sum[j].w += v[u][j].w;
-              }
+              for (int j = 0; j < kE; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  sum[j][h].x += v[u][j][h].x;
+                  sum[j][h].y += v[u][j][h].y;
+                  sum[j][h].z += v[u][j][h].z;
+                  sum[j][h].w += v[u][j][h].w;
+                }
+            }
           }
 #pragma unroll
           for (int j = 0; j < kE; ++j) {
-            const int e = e0 + j * kFp8EpiWarps * 32;
-            if (e >= total) break;
-            const int r = e / kQ, n = ntile * C::NT + (e - r * kQ) * 4;
+            const int e = e0 + j * kStep;
+            const int r = e % kFp8Rows, n = ntile * C::NT + e / kFp8Rows * 8;
+            if (r >= rows) continue;
             uint16_t* y = a.Y + static_cast<size_t>(m0 + r) * a.N + n;
-            if (a.vec && n + 4 <= a.N) {
-              *reinterpret_cast<uint2*>(y) =
-                  make_uint2(bf16_pack2(sum[j].x, sum[j].y), bf16_pack2(sum[j].z, sum[j].w));
+            const float o[8] = {sum[j][0].x, sum[j][0].y, sum[j][0].z, sum[j][0].w,
+                                sum[j][1].x, sum[j][1].y, sum[j][1].z, sum[j][1].w};
+            if (a.vec && n + 8 <= a.N) {
+              *reinterpret_cast<uint4*>(y) = make_uint4(bf16_pack2(o[0], o[1]), bf16_pack2(o[2], o[3]),
+                                                        bf16_pack2(o[4], o[5]), bf16_pack2(o[6], o[7]));
             } else {
-              const float s4[4] = {sum[j].x, sum[j].y, sum[j].z, sum[j].w};
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (n + i < a.N) y[i] = __bfloat16_as_ushort(__float2bfloat16_rn(s4[i]));
+              for (int i = 0; i < 8; ++i)
+                if (n + i < a.N) y[i] = __bfloat16_as_ushort(__float2bfloat16_rn(o[i]));
             }
           }
-        };
-        if (total <= 2 * kFp8EpiWarps * 32) {
-          for (int e = tid; e < total; e += kFp8EpiWarps * 32)
-            sum_of(std::integral_constant<int, 1>{}, std::integral_constant<int, 8>{}, e);
-        } else {
-          for (int e = tid; e < total; e += 4 * kFp8EpiWarps * 32)
-            sum_of(std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{}, e);
         }
       }
     }
@@ -577,17 +545,11 @@ __global__ void __launch_bounds__(C::kThreads, 1)
 
   if (warp >= 4 && lane == 0) bulk_wait_all();  // output copies are complete
   tc_fence_before();
-  if constexpr (C::PAIR)
-    cluster_sync();  // neither CTA leaves while the other may reach its memory
-  else
-    __syncthreads();
+  cluster_sync();  // neither CTA leaves while the other may reach its memory
   if (warp == 1) {
     mbar_wait(done, 0);  // every issued MMA has completed
     tc_fence_after();
-    if constexpr (C::PAIR)
-      tmem_dealloc_pair(tmem, C::kTmemCols);
-    else
-      tmem_dealloc(tmem, C::kTmemCols);
+    tmem_dealloc_pair(tmem, 512);
   }
 }
 
