@@ -269,6 +269,11 @@ __device__ __forceinline__ unsigned ld_acquire_gpu(const unsigned int* p) {
   asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
   return v;
 }
+// Add without waiting for the old value; publishes this thread's earlier writes
+// and, through a barrier before it, those of its CTA.
+__device__ __forceinline__ void red_add_release_gpu(unsigned int* p, unsigned int v) {
+  asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
 __device__ __forceinline__ void fence_proxy_async_all() {
   asm volatile("fence.proxy.async;" ::: "memory");
 }
@@ -630,7 +635,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks)
     // publish: ordinary stores, read elsewhere by tensor copies and loads
     fence_proxy_async_all();
     __syncthreads();
-    if (threadIdx.x == 0) atom_add_acq_rel_gpu(&a.cnt->h_done, 1u);
+    if (threadIdx.x == 0) red_add_release_gpu(&a.cnt->h_done, 1u);
   } else if (down) {
     const int q0 = 32 * rank / kMoeCluster, w = 32 / kMoeCluster;  // in units of 4 columns
     const uint32_t mine = smem_u32(sums);
