@@ -95,7 +95,8 @@ __device__ __forceinline__ uint32_t half_warp_max(uint32_t a) {
 // Half a warp per (token, 128 channels): 8 channels per lane, one 16-byte
 // load and one 8-byte store, U blocks in flight.  K % 16 == 0; with RAGGED the
 // last block of a row is shorter (lanes past K hold nothing), without it the
-// blocks are simply consecutive.
+// blocks are simply consecutive.  Bound by instruction issue: 4099 x 13824 in
+// 45 us, 3.8 TB/s (U = 1: 53 us, U = 4: 58 us, fewer warps resident).
 template <int U, bool RAGGED>
 __global__ void __launch_bounds__(256) fp8_quantize_x_kernel(const uint16_t* X, long long blocks,
                                                              int K, FastDivIdx by_kb, uint8_t* q,
@@ -141,7 +142,8 @@ __global__ void __launch_bounds__(256) fp8_quantize_x_kernel(const uint16_t* X, 
 // ----------------------------------------------------------------- weights
 // One CTA per 128 x 128 block of one of B matrices: 16 lanes per row, 8
 // channels per lane, 16 rows at a time; the values stay in registers between
-// the maximum and the codes.
+// the maximum and the codes.  Bound by HBM: 16 x 2000 x 4096 in 111 us, 5.9 TB/s
+// (with 2 CTAs per SM instead of 3: 130 us; 4, which spills: 142 us).
 __global__ void __launch_bounds__(256, 3) fp8_quantize_w_kernel(const float* W, int N, int K,
                                                              uint8_t* q, float* s) {
   __shared__ uint32_t wmax[8];
@@ -194,7 +196,8 @@ __global__ void __launch_bounds__(256, 3) fp8_quantize_w_kernel(const float* W, 
 // y = r * rsqrt(mean + eps) * w in fp32 and its codes without a rounding in
 // between.  residual_out is bf16(r); the norm itself uses the unrounded sum.
 // Every thread reads its own channels before it writes them, so residual_out
-// may be residual or x.
+// may be residual or x.  Bound by HBM: 8191 x 8192 with every output in 99 to
+// 103 us, 5.9 to 6.1 TB/s; one row of 4096 in 2.4 us, the launch.
 template <int CPT>
 __global__ void __launch_bounds__(1024) fp8_add_rmsnorm_kernel(
     const uint16_t* x, const uint16_t* residual, const uint16_t* __restrict__ weight, float eps,

