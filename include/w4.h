@@ -490,13 +490,15 @@ w4_status fp8_add_rmsnorm(const uint16_t* X, const uint16_t* residual, const uin
  * exact).
  *   qx, sx     in   e4m3 [M, K] (16-byte aligned), fp32 [M, KB]
  *   qw, sw     in   e4m3 [N, K] (16-byte aligned), fp32 [ceil(N / 128), KB]
- *   M, N       1..2^24
+ *   M, N, K    M, N <= 2^24, K <= 2^20, M K and N K < 2^40, M N < 2^39: larger
+ *              returns W4_ERR_UNSUPPORTED, launching nothing
  *   Y          out  bf16 [M, N]
  *   workspace  at least fp8_gemm_workspace_bytes(M, N, K) bytes (0 for an
- *              invalid shape), 256-byte aligned, ZEROED ONCE before its first
+ *              invalid or unsupported shape), 256-byte aligned, ZEROED ONCE before its first
  *              use; the call leaves its counters (the first 262144 bytes)
  *              zeroed, so calls of any shape, and w4a16_gemm / nf4_gemm, may
- *              share it as long as they are ordered on one stream.
+ *              share it as long as they are ordered on one stream.  After
+ *              W4_ERR_TIMEOUT it must be zeroed again.
  * As in w4a16_gemm the weights (qw, sw) are constant model state: they are
  * read before the kernel before this one on the stream has finished, and must
  * not be written by it (fp8_quantize_weights directly before is fine).      */
@@ -518,11 +520,11 @@ w4_status fp8_gemm(const uint8_t* qx, const float* sx, const uint8_t* qw, const 
  *   w13, s13   in   e4m3 [E, 2, I, H] (gate, up), fp32 [E, 2, ceil(I/128), ceil(H/128)]
  *   w2, s2     in   e4m3 [E, H, I], fp32 [E, ceil(H/128), ceil(I/128)]
  *              (fp8_quantize_weights with B = 2 E and B = E)
- *   top        1..min(E, 16);  H, I multiples of 16, at most 2^20
+ *   top        1..min(E, 16);  H, I multiples of 16, at most 2^19
  *   Y          out  bf16 [T, H];  ids  out  int32 [T, top];  weights  out  fp32 [T, top]
  *   workspace  as for fp8_gemm, fp8_moe_workspace_bytes(T, E, top, H, I) bytes
- * T, E or top above the limits: W4_ERR_UNSUPPORTED.  X, router, w13, w2 are
- * 16-byte aligned.  A token whose logits are all NaN is given experts
+ * T, E, top, H or I above the limits: W4_ERR_UNSUPPORTED (workspace size 0).
+ * X, router, w13, w2 are 16-byte aligned.  More tokens: fp8_gemm per expert.  A token whose logits are all NaN is given experts
  * 0..top-1 and a NaN output.                                                */
 size_t fp8_moe_workspace_bytes(int T, int E, int top, int H, int I);
 w4_status fp8_moe(const uint16_t* X, const uint16_t* router, const uint8_t* w13, const float* s13,

@@ -58,7 +58,7 @@ INVALID = {
     "gemm no workspace": lambda L: L.fp8_gemm(P, P, P, P, 1, 4, 128, P, None, WS, None),
     "gemm small workspace": lambda L: L.fp8_gemm(P, P, P, P, 1, 4, 128, P, P, 256, None),
     "gemm K % 16": lambda L: L.fp8_gemm(P, P, P, P, 1, 4, 100, P, P, WS, None),
-    "gemm M": lambda L: L.fp8_gemm(P, P, P, P, 1 << 25, 4, 128, P, P, WS, None),
+    "gemm M 0": lambda L: L.fp8_gemm(P, P, P, P, 0, 4, 128, P, P, WS, None),
     "gemm alignment": lambda L: L.fp8_gemm(P, P, ODD, P, 1, 4, 128, P, P, WS, None),
     "gemm Y alignment": lambda L: L.fp8_gemm(P, P, P, P, 1, 4, 128, BYTE, P, WS, None),
     "moe null": lambda L: L.fp8_moe(P, P, P, P, P, None, 1, 8, 2, 128, 128, 1, P, P, P, P, WS, None),
@@ -83,6 +83,11 @@ UNSUPPORTED = {
     "moe T": lambda L: L.fp8_moe(P, P, P, P, P, P, 129, 8, 2, 128, 128, 1, P, P, P, P, WS, None),
     "moe E": lambda L: L.fp8_moe(P, P, P, P, P, P, 1, 513, 2, 128, 128, 1, P, P, P, P, WS, None),
     "moe top": lambda L: L.fp8_moe(P, P, P, P, P, P, 1, 64, 17, 128, 128, 1, P, P, P, P, WS, None),
+    "moe H": lambda L: L.fp8_moe(P, P, P, P, P, P, 1, 8, 2, 1 << 20, 128, 1, P, P, P, P, WS, None),
+    "gemm M": lambda L: L.fp8_gemm(P, P, P, P, 1 << 25, 4, 128, P, P, WS, None),
+    "gemm K": lambda L: L.fp8_gemm(P, P, P, P, 1, 4, 1 << 21, P, P, WS, None),
+    "gemm N K": lambda L: L.fp8_gemm(P, P, P, P, 1, 1 << 21, 1 << 19, P, P, WS, None),
+    "gemm M N": lambda L: L.fp8_gemm(P, P, P, P, 1 << 20, 1 << 19, 128, P, P, WS, None),
     "weights blocks": lambda L: L.fp8_quantize_weights(P, 1 << 20, 1 << 18, 4096, P, P, None),
 }
 
@@ -97,6 +102,7 @@ def test_workspace_sizes():
     assert L.fp8_gemm_workspace_bytes(1, 4096, 4096) >= 65536 * 4
     assert L.fp8_gemm_workspace_bytes(0, 4096, 4096) == 0
     assert L.fp8_gemm_workspace_bytes(1, 4096, 100) == 0
+    assert L.fp8_gemm_workspace_bytes(1, 4096, 1 << 21) == 0
     assert L.fp8_moe_workspace_bytes(1, 8, 2, 4096, 1024) > 65536 * 4
     assert L.fp8_moe_workspace_bytes(129, 8, 2, 4096, 1024) == 0
     assert L.fp8_moe_workspace_bytes(1, 8, 9, 4096, 1024) == 0

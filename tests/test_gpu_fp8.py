@@ -189,6 +189,8 @@ GEMM = [
     (64, 260, 8192), (65, 129, 256), (100, 640, 2048), (127, 384, 1024), (128, 1024, 4096),
     (129, 512, 2048), (200, 1000, 656), (256, 2304, 1024), (300, 20000, 512), (511, 768, 5120),
     (1000, 1000, 1008), (1025, 2050, 272),
+    # more tokens: cut tails with odd rows and columns, 128- and 256-row tiles
+    (257, 1001, 14336), (400, 6001, 4096), (700, 259, 9008), (300, 9473, 1040),
 ]
 
 
@@ -448,6 +450,36 @@ def test_layer_captured_in_graphs(w4):
         torch.cuda.synchronize()
         for o, e in zip(outs, eager):
             assert torch.equal(o[0], e[0]) and torch.equal(o[1], e[1])
+    ok(w4)
+
+
+def test_large_product_captured_and_eager(w4):
+    # a product with partial sums: two graphs of it replayed at once beside
+    # eager calls, and the eager default workspace stays clean
+    M, N, K = 300, 600, 16384
+    ins = []
+    for seed in (1, 2):
+        qx, sx = w4.fp8_quantize_activations(x_dev(draw_x(M, K, seed)))
+        qw, sw = w4.fp8_quantize_weights(dev(S.draw_w(N, K, 0.02, seed=seed, tag=88)))
+        ins.append((qx, sx, qw, sw))
+    assert w4.lib.fp8_gemm_workspace_bytes(M, N, K) > 65536 * 4
+    eager = [w4.fp8_gemm(*a) for a in ins]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for a in ins:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(w4.fp8_gemm(*a))
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in ins]
+    for _ in range(5):
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+        again = [w4.fp8_gemm(*a) for a in ins]
+        torch.cuda.synchronize()
+        for o, e, v in zip(outs, eager, again):
+            assert torch.equal(o, e) and torch.equal(v, e)
     ok(w4)
 
 

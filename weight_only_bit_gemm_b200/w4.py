@@ -580,7 +580,8 @@ def _fp8_workspace(need, workspace, like, dev, stream):
         buf = workspace
     elif torch.cuda.is_current_stream_capturing():
         buf = torch.empty(need + 256, dtype=torch.uint8, device=like.device)
-        buf[:_FP8_COUNTER_BYTES + 256].zero_()
+        if need > _FP8_COUNTER_BYTES:  # (a call without partial sums counts nothing)
+            buf[:_FP8_COUNTER_BYTES + 256].zero_()
     else:
         buf = _FP8_WS.get((dev, stream))
         if buf is None or buf.numel() < need + 256:
@@ -648,7 +649,9 @@ def fp8_add_rmsnorm(X, weight, residual=None, eps=1e-6, want_y=False, residual_o
 
 def fp8_gemm(qx, sx, qw, sw, out=None, workspace=None):
     """bf16 Y[M, N] = (qx sx) . (qw sw)^T for codes and scales as
-    fp8_quantize_activations / fp8_add_rmsnorm and fp8_quantize_weights give them."""
+    fp8_quantize_activations / fp8_add_rmsnorm and fp8_quantize_weights give them.
+    The weights are constant model state: another library's kernel that writes
+    them must have finished before this call (see w4.h)."""
     dev = _fp8_first(qx, _E4M3, 2, "qx")
     M, K = qx.shape
     N = qw.shape[0]
@@ -659,7 +662,9 @@ def fp8_gemm(qx, sx, qw, sw, out=None, workspace=None):
     out = _fp8_out(out, (M, N), qx, dev)
     need = lib.fp8_gemm_workspace_bytes(M, N, K)
     if need == 0:
-        raise W4Error(W4_ERR_INVALID_ARG, "fp8_gemm_workspace_bytes")
+        valid = M >= 1 and N >= 1 and K >= 16 and K % 16 == 0
+        raise W4Error(W4_ERR_UNSUPPORTED if valid else W4_ERR_INVALID_ARG,
+                      "fp8_gemm_workspace_bytes")
     stream = _raw_stream(dev)
     ws, ws_bytes = _fp8_workspace(need, workspace, qx, dev, stream)
     _check(lib.fp8_gemm(qx.data_ptr(), s1, w, s2, M, N, K, out.data_ptr(), ws, ws_bytes, stream),
@@ -685,7 +690,7 @@ def fp8_moe(X, router, w13, s13, w2, s2, top_k, renormalize=True, out=None, work
     q2 = _fp8_arg(s2, _F32, (E, hb, ib), dev, "s2")
     need = lib.fp8_moe_workspace_bytes(T, E, top_k, H, I)
     if need == 0:
-        supported = T <= 128 and E <= 512 and top_k <= 16
+        supported = T <= 128 and E <= 512 and top_k <= 16 and H <= 1 << 19 and I <= 1 << 19
         raise W4Error(W4_ERR_INVALID_ARG if supported else W4_ERR_UNSUPPORTED,
                       "fp8_moe_workspace_bytes")
     out = _fp8_out(out, (T, H), X, dev)
