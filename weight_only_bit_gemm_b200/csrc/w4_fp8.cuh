@@ -55,33 +55,62 @@ __device__ __forceinline__ void unpack_bf16x8(uint4 w, float (&v)[8]) {
   }
 }
 
-// v / s rounded to nearest for a divisor shared by many values, r = 1 / s
-// rounded to nearest (Markstein, "Computation of elementary functions on the
-// IBM RISC System/6000 processor", 1990: with such an r, and q within one ulp
-// of the quotient, q + r (v - q s) in two fused operations is the correctly
-// rounded quotient).  v r alone can be 1.5 ulp off, so the first step brings q
-// within one ulp and the second rounds correctly.  Needs a normal r and no
-// harmful underflow in v - q s: s >= 1e-25, and then a value so small that its
-// remainder is inexact has the code 0 in any case.
-__device__ __forceinline__ float div_by(float v, float s, float r) {  // s > 0
-  const float q0 = v * r;
-  const float q1 = fmaf(fmaf(-q0, s, v), r, q0);
-  return copysignf(fmaf(fmaf(-q1, s, v), r, q1), v);  // (a zero keeps its sign)
+// Two floats as one operand of the two-wide fp32 instructions.
+__device__ __forceinline__ unsigned long long f32x2(float lo, float hi) {
+  unsigned long long d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ unsigned long long fma_f32x2(unsigned long long a, unsigned long long b,
+                                                        unsigned long long c) {
+  unsigned long long d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ unsigned long long mul_f32x2(unsigned long long a, unsigned long long b) {
+  unsigned long long d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
 
-// Codes of 8 values: two words.  (An IEEE division per value costs more
-// instructions than HBM speed leaves, about 16 per value at 3 bytes.)
-__device__ __forceinline__ uint2 fp8_codes8(const float (&v)[8], float s) {
+// Codes of -u / s for 8 values u: two words.  An IEEE division per value costs
+// more instructions than HBM speed leaves (about 16 per value at 3 bytes).
+// The divisor is shared, so its reciprocal r, rounded to nearest, is taken
+// once (Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", 1990: with such an r, and q within one ulp of v / s,
+// q - r (q s - v) in two fused operations is the correctly rounded quotient).
+// v r alone can be 1.5 ulp off, so a first step brings q within one ulp and
+// the second rounds correctly.  This needs a normal r and no harmful underflow
+// in q s - v: s >= 1e-25, and then a value so small that its remainder is
+// inexact has the code 0 in any case.  With u = -v every step is one two-wide
+// fma, q s + u and (q s + u) (-r) + q, and a zero keeps its sign.
+__device__ __forceinline__ uint2 fp8_codes8_neg(const float (&u)[8], float s) {
   uint32_t c[4];
   if (s >= 1e-25f) {
     const float r = __frcp_rn(s);
+    const unsigned long long s2 = f32x2(s, s), nr2 = f32x2(-r, -r);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = e4m3x2(div_by(v[2 * i], s, r), div_by(v[2 * i + 1], s, r));
+    for (int i = 0; i < 4; ++i) {
+      const unsigned long long u2 = f32x2(u[2 * i], u[2 * i + 1]);
+      unsigned long long q = mul_f32x2(u2, nr2);
+      q = fma_f32x2(fma_f32x2(q, s2, u2), nr2, q);
+      q = fma_f32x2(fma_f32x2(q, s2, u2), nr2, q);
+      float lo, hi;
+      asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(q));
+      c[i] = e4m3x2(lo, hi);
+    }
   } else {  // tiny, or NaN
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = e4m3x2(__fdiv_rn(v[2 * i], s), __fdiv_rn(v[2 * i + 1], s));
+    for (int i = 0; i < 4; ++i)
+      c[i] = e4m3x2(__fdiv_rn(-u[2 * i], s), __fdiv_rn(-u[2 * i + 1], s));
   }
   return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+
+// 8 bf16 values of a 16-byte load, widened and negated.
+__device__ __forceinline__ void unpack_neg_bf16x8(uint4 w, float (&u)[8]) {
+  constexpr uint32_t kSigns = 0x80008000u;
+  unpack_bf16x8(make_uint4(w.x ^ kSigns, w.y ^ kSigns, w.z ^ kSigns, w.w ^ kSigns), u);
 }
 
 // Largest |v| bits over the 16 lanes of this half warp.
@@ -91,12 +120,21 @@ __device__ __forceinline__ uint32_t half_warp_max(uint32_t a) {
   return a;
 }
 
+// Largest |v| of 8 bf16 values, as fp32 bits.  The magnitudes' patterns order
+// as integers, two to a word.
+__device__ __forceinline__ uint32_t abs_max_bf16x8(uint4 w) {
+  constexpr uint32_t kMag = 0x7FFF7FFFu;
+  const uint32_t m = __vmaxu2(__vmaxu2(w.x & kMag, w.y & kMag), __vmaxu2(w.z & kMag, w.w & kMag));
+  return max(m << 16, m & 0xFFFF0000u);
+}
+
 // ------------------------------------------------------------- activations
 // Half a warp per (token, 128 channels): 8 channels per lane, one 16-byte
 // load and one 8-byte store, U blocks in flight.  K % 16 == 0; with RAGGED the
 // last block of a row is shorter (lanes past K hold nothing), without it the
 // blocks are simply consecutive.  Bound by instruction issue: 4099 x 13824 in
-// 45 us, 3.8 TB/s (U = 1: 53 us, U = 4: 58 us, fewer warps resident).
+// 40 us, 4.3 TB/s (with one-wide fp32 arithmetic and U = 2 45 us, U = 1 53 us,
+// U = 4 58 us).
 template <int U, bool RAGGED>
 __global__ void __launch_bounds__(256) fp8_quantize_x_kernel(const uint16_t* X, long long blocks,
                                                              int K, FastDivIdx by_kb, uint8_t* q,
@@ -126,13 +164,10 @@ __global__ void __launch_bounds__(256) fp8_quantize_x_kernel(const uint16_t* X, 
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      float v[8];
-      unpack_bf16x8(w[u], v);
-      uint32_t mx = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) mx = max(mx, abs_bits(v[i]));
-      const float sc = fp8_scale(half_warp_max(mx));
-      if (have[u]) *reinterpret_cast<uint2*>(q + at[u]) = fp8_codes8(v, sc);
+      float v[8];  // negated
+      unpack_neg_bf16x8(w[u], v);
+      const float sc = fp8_scale(half_warp_max(abs_max_bf16x8(w[u])));
+      if (have[u]) *reinterpret_cast<uint2*>(q + at[u]) = fp8_codes8_neg(v, sc);
       const long long b = b0 + u * step + threadIdx.x / 16;
       if (l == 0 && b < blocks) s[b] = sc;
     }
@@ -140,13 +175,16 @@ __global__ void __launch_bounds__(256) fp8_quantize_x_kernel(const uint16_t* X, 
 }
 
 // ----------------------------------------------------------------- weights
+constexpr int kFp8WThreads = 256, kFp8WBlocks = 3;
+
 // One CTA per 128 x 128 block of one of B matrices: 16 lanes per row, 8
 // channels per lane, 16 rows at a time; the values stay in registers between
-// the maximum and the codes.  Bound by HBM: 16 x 2000 x 4096 in 111 us, 5.9 TB/s
-// (with 2 CTAs per SM instead of 3: 130 us; 4, which spills: 142 us).
-__global__ void __launch_bounds__(256, 3) fp8_quantize_w_kernel(const float* W, int N, int K,
+// the maximum and the codes.  Bound by HBM: 16 x 2000 x 4096 in 115 us, 5.7 TB/s
+// (2 CTAs per SM 126 us; CTAs of 512 threads, 2 per SM, 119 us).
+__global__ void __launch_bounds__(kFp8WThreads, kFp8WBlocks) fp8_quantize_w_kernel(const float* W, int N, int K,
                                                              uint8_t* q, float* s) {
-  __shared__ uint32_t wmax[8];
+  constexpr int kRows = kFp8WThreads / 16, kTurns = kFp8Block / kRows;
+  __shared__ uint32_t wmax[kFp8WThreads / 32];
   const uint32_t kb_n = (K + kFp8Block - 1) / kFp8Block, nb_n = (N + kFp8Block - 1) / kFp8Block;
   const uint32_t bn = blockIdx.x / kb_n, kb = blockIdx.x - bn * kb_n;
   const uint32_t mat = bn / nb_n;
@@ -154,11 +192,11 @@ __global__ void __launch_bounds__(256, 3) fp8_quantize_w_kernel(const float* W, 
   const int l = threadIdx.x & 15, r0 = threadIdx.x >> 4;
   const int k = static_cast<int>(kb) * kFp8Block + l * 8;
   const float* Wm = W + static_cast<size_t>(mat) * N * K;
-  float v[8][8];
+  float v[kTurns][8];
   uint32_t mx = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int n = nb * kFp8Block + r0 + 16 * i;
+  for (int i = 0; i < kTurns; ++i) {
+    const int n = nb * kFp8Block + r0 + kRows * i;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
     if (n < N && k < K) {
       const float4* p = reinterpret_cast<const float4*>(Wm + static_cast<size_t>(n) * K + k);
@@ -176,14 +214,17 @@ __global__ void __launch_bounds__(256, 3) fp8_quantize_w_kernel(const float* W, 
   __syncthreads();
   mx = wmax[0];
 #pragma unroll
-  for (int i = 1; i < 8; ++i) mx = max(mx, wmax[i]);
+  for (int i = 1; i < kFp8WThreads / 32; ++i) mx = max(mx, wmax[i]);
   const float sc = fp8_scale(mx);
   uint8_t* qm = q + static_cast<size_t>(mat) * N * K;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int n = nb * kFp8Block + r0 + 16 * i;
+  for (int i = 0; i < kTurns; ++i) {
+    const int n = nb * kFp8Block + r0 + kRows * i;
+    float u[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) u[j] = -v[i][j];
     if (n < N && k < K)
-      *reinterpret_cast<uint2*>(qm + static_cast<size_t>(n) * K + k) = fp8_codes8(v[i], sc);
+      *reinterpret_cast<uint2*>(qm + static_cast<size_t>(n) * K + k) = fp8_codes8_neg(u, sc);
   }
   if (threadIdx.x == 0) s[blockIdx.x] = sc;
   // a product launched next may read the weights before this grid has ended
@@ -196,8 +237,8 @@ __global__ void __launch_bounds__(256, 3) fp8_quantize_w_kernel(const float* W, 
 // y = r * rsqrt(mean + eps) * w in fp32 and its codes without a rounding in
 // between.  residual_out is bf16(r); the norm itself uses the unrounded sum.
 // Every thread reads its own channels before it writes them, so residual_out
-// may be residual or x.  Bound by HBM: 8191 x 8192 with every output in 99 to
-// 103 us, 5.9 to 6.1 TB/s; one row of 4096 in 2.4 us, the launch.
+// may be residual or x.  Bound by HBM: 8191 x 8192 with every output in 97
+// us, 6.2 TB/s; one row of 4096 in 2.4 us, the launch.
 template <int CPT>
 __global__ void __launch_bounds__(1024) fp8_add_rmsnorm_kernel(
     const uint16_t* x, const uint16_t* residual, const uint16_t* __restrict__ weight, float eps,
@@ -253,7 +294,7 @@ __global__ void __launch_bounds__(1024) fp8_add_rmsnorm_kernel(
     uint32_t mx = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      v[c][j] = v[c][j] * rstd * w8[j];
+      v[c][j] = v[c][j] * -rstd * w8[j];  // -y
       mx = max(mx, abs_bits(v[c][j]));
     }
     if (!have) mx = 0;  // 0 * rstd is NaN where rstd is not finite
@@ -264,11 +305,11 @@ __global__ void __launch_bounds__(1024) fp8_add_rmsnorm_kernel(
       uint32_t p[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        p[j] = static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(v[c][2 * j]))) |
-               (static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(v[c][2 * j + 1]))) << 16);
+        p[j] = static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(-v[c][2 * j]))) |
+               (static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(-v[c][2 * j + 1]))) << 16);
       *reinterpret_cast<uint4*>(y_out + row + k) = make_uint4(p[0], p[1], p[2], p[3]);
     }
-    *reinterpret_cast<uint2*>(q + row + k) = fp8_codes8(v[c], sc);
+    *reinterpret_cast<uint2*>(q + row + k) = fp8_codes8_neg(v[c], sc);
     if ((threadIdx.x & 15) == 0) s[static_cast<size_t>(blockIdx.x) * kb_n + k / kFp8Block] = sc;
   }
 }

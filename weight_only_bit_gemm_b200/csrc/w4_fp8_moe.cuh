@@ -92,14 +92,12 @@ __global__ void __launch_bounds__(256) moe_route_kernel(const MoeArgs a) {
     const bool live = b < a.T * a.HB;
     const int m = live ? b / a.HB : 0, k = (b - m * a.HB) * kFp8Block + l * 8;
     const bool have = live && k < a.H;
-    float v[8] = {};
     const size_t at = static_cast<size_t>(m) * a.H + k;
-    if (have) unpack_bf16x8(__ldcg(reinterpret_cast<const uint4*>(a.X + at)), v);
-    uint32_t mx = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) mx = max(mx, abs_bits(v[i]));
-    const float sc = fp8_scale(half_warp_max(mx));
-    if (have) *reinterpret_cast<uint2*>(a.xq + at) = fp8_codes8(v, sc);
+    const uint4 w = have ? __ldcg(reinterpret_cast<const uint4*>(a.X + at)) : make_uint4(0u, 0u, 0u, 0u);
+    float v[8];  // negated
+    unpack_neg_bf16x8(w, v);
+    const float sc = fp8_scale(half_warp_max(abs_max_bf16x8(w)));
+    if (have) *reinterpret_cast<uint2*>(a.xq + at) = fp8_codes8_neg(v, sc);
     if (live && l == 0) a.sx[b] = sc;
     return;
   }
