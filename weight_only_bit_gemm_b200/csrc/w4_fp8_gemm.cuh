@@ -3,8 +3,8 @@
 // for e4m3 codes, on the tensor cores (tcgen05.mma kind::f8f6f4).
 //
 // The scales change every 128 channels, so the tensor-memory accumulator
-// holds one block's sum at a time: four MMAs of K = 32 fill one of two
-// accumulator buffers while the epilogue warps read the other and add
+// holds one block's sum at a time: four MMAs of K = 32 fill one
+// accumulator buffer while the epilogue warps read another and add
 //   acc += (sx sw) * block sum
 // to fp32 registers, one fma per output and block.  Tokens are the MMA's rows
 // (tensor-memory lanes) and weight rows its columns: a thread then owns one
@@ -23,9 +23,8 @@
 //
 // More tokens (fp8_tc_gemm_kernel): CTA pairs (cta_group::2) of 256 tokens x
 // 256 or 128 weight rows, each CTA staging half of each operand, in a
-// persistent grid.  Each worker (CTA or pair) takes whole tiles while
-// every worker gets one; the tiles left over are cut along K into equal runs
-// of blocks, one per worker, whose fp32 partial sums the last run of a tile
+// persistent grid.  Each pair takes whole tiles while every pair gets one; the
+// tiles left over stay whole or are cut along K into equal runs of blocks, whose fp32 partial sums the last run of a tile
 // to finish adds in the order of K (the result does not depend on which
 // that is).
 //
@@ -37,8 +36,6 @@
 #pragma once
 
 #include <cuda_bf16.h>
-
-#include <type_traits>
 
 #include "w4_fp8.cuh"
 
@@ -82,7 +79,7 @@ struct Fp8GemmArgs {
   unsigned int* counter;  // [tail tile (and CTA of a pair)], zero between calls
   int M, N, KB, NB;
   int tiles_m, tiles_n, group_m;
-  int workers;            // CTAs or pairs
+  int workers;            // pairs
   int rounds;             // whole tiles per worker
   int tail;               // tiles left over, the last ones
   int tail_workers;       // runs they are cut into (0: each whole, one worker each)
