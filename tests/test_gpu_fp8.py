@@ -532,3 +532,84 @@ def test_moe_refusals(w4):
         run_moe(w4, big, 1, True)
     assert e.value.status == w4.W4_ERR_UNSUPPORTED
     ok(w4)
+
+
+# ------------------------------------------------- offsets beyond 32 bits
+
+def big_bf16(M, K, seed):
+    """[M, K] on the GPU: one drawn block of rows repeated, so that any row's
+    expectation is cheap."""
+    base = draw_x(97, K, seed)
+    x = x_dev(base)
+    return x.repeat(-(-M // 97), 1)[:M].contiguous(), base
+
+
+def test_more_than_2_31_activations(w4):
+    M, K = 66001, 32800                                  # 2.16e9 values
+    x, base = big_bf16(M, K, 91)
+    q, s = w4.fp8_quantize_activations(x)
+    ok(w4)
+    rows = [0, 40000, M - 1]
+    qr, sr = O.fp8_quantize_rows(f32(base[[r % 97 for r in rows]]))
+    assert np.array_equal(codes(q[rows]), qr)
+    same_scales(s[rows].cpu().numpy(), sr)
+    w = torch.ones(K, dtype=torch.bfloat16, device="cuda")
+    qn, sn, ro, _ = w4.fp8_add_rmsnorm(x, w, x)
+    ok(w4)
+    # the same rows in a small call: the same bits
+    q1, s1, r1, _ = w4.fp8_add_rmsnorm(x[rows].contiguous(), w, x[rows].contiguous())
+    assert np.array_equal(codes(qn[rows]), codes(q1)) and torch.equal(sn[rows], s1)
+    assert torch.equal(ro[rows], r1)
+
+
+def test_more_than_2_31_weights(w4):
+    B, N, K = 3, 22001, 32784                            # 2.16e9 values
+    W = torch.empty(B, N, K, device="cuda").normal_(std=0.02)
+    q, s = w4.fp8_quantize_weights(W)
+    ok(w4)
+    part = W[2, 21888:, 32640:].cpu().numpy()            # the last blocks of the last matrix
+    qr, sr = O.fp8_quantize_blocks(part)
+    assert np.array_equal(codes(q[2, 21888:, 32640:].contiguous()), qr)
+    same_scales(s[2, -1:, -2:].cpu().numpy(), sr)
+
+
+def test_more_than_2_31_outputs(w4):
+    M, N, K = 66001, 32808, 144                          # 2.17e9 outputs
+    x, base = big_bf16(M, K, 92)
+    qx, sx = w4.fp8_quantize_activations(x)
+    qw, sw = draw_q(N, K, 93)
+    y = w4.fp8_gemm(qx, sx, q_dev(qw), dev(sw))
+    ok(w4)
+    rows = [0, 40000, M - 1]
+    ref, absum = O.fp8_gemm_ref(codes(qx[rows]), sx[rows].cpu().numpy(), qw, sw)
+    assert (np.abs(f64(y[rows]) - ref) <= O.fp8_gemm_tolerance(ref, absum, K)).all()
+
+
+def test_back_to_back_calls_on_reused_memory(w4):
+    # every call starts while the one before it runs, and the allocator hands the
+    # same memory to the next turn's codes and scales: no turn may see another's
+    sets = [layer_inputs(T, 512, 272, 8, 40 + T) for T in (3, 3 + 32, 3 + 64)]
+    alone = []
+    for a in sets:
+        alone.append(layer(w4, *a)[:2])
+        torch.cuda.synchronize()
+    big = []
+    for seed in (1, 2):
+        x = x_dev(draw_x(160, 1040, seed))
+        qw, sw = w4.fp8_quantize_weights(dev(S.draw_w(700, 1040, 0.02, seed=seed, tag=89)))
+        torch.cuda.synchronize()
+        y = w4.fp8_gemm(*w4.fp8_quantize_activations(x), qw, sw)
+        torch.cuda.synchronize()
+        big.append((x, qw, sw, y))
+    got = []
+    for turn in range(60):
+        got.append([layer(w4, *a)[:2] for a in sets])
+        for x, qw, sw, y in big:
+            got[-1].append((w4.fp8_gemm(*w4.fp8_quantize_activations(x), qw, sw),))
+    torch.cuda.synchronize()
+    ok(w4)
+    for turn in got:
+        for g, e in zip(turn[:3], alone):
+            assert torch.equal(g[0], e[0]) and torch.equal(g[1], e[1])
+        for g, b in zip(turn[3:], big):
+            assert torch.equal(g[0], b[3])
