@@ -1,0 +1,47 @@
+"""Rules of the kernel sources that no run can show (no GPU needed)."""
+import glob
+import os
+import re
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                    "weight_only_bit_gemm_b200", "csrc")
+
+
+def source(name):
+    text = open(os.path.join(CSRC, name)).read()
+    return re.sub(r"//[^\n]*", "", text)
+
+
+def body(text, head):
+    """The braces' content after the first match of head."""
+    at = text.index("{", re.search(head, text).end())
+    depth = 0
+    for i in range(at, len(text)):
+        depth += {"{": 1, "}": -1}.get(text[i], 0)
+        if depth == 0:
+            return text[at:i + 1]
+    raise AssertionError(head)
+
+
+@pytest.mark.parametrize("name", sorted(os.path.basename(p) for p in glob.glob(CSRC + "/*")))
+def test_no_branch_on_a_lanes_own_answer_is_declared_uniform(name):
+    assert not re.search(r"@!?\w+\s+bra\.uni", source(name))
+
+
+def test_warps_are_whole_at_their_barriers():
+    # instructions of whole warps (.aligned) reached by lanes that took
+    # different ways: the warp's lanes meet first
+    assert "__syncwarp();" in body(source("w4_ptx.cuh"), r"void cluster_sync\(\)")
+    assert "__syncwarp();" in body(source("w4_fp8_gemm.cuh"), r"void epi_sync\(\)")
+    for name in ("w4_fp8_gemm.cuh", "w4_fp8_moe.cuh"):
+        text = source(name)
+        # a wait that is skipped after an earlier one gave up
+        skipped = re.findall(r"if \(ok\)\s*ok = mbar_wait_warp\([^;]*;\s*(\w+)\s*(\w*)", text)
+        assert skipped and all(s == ("else", "__syncwarp") for s in skipped)
+        # per-lane waits directly before the tensor memory is freed
+        assert not re.search(r"[^_]mbar_wait\(done", text)
+    # a vote orders no memory: the lanes that did not wait for h themselves
+    moe = source("w4_fp8_moe.cuh")
+    assert re.search(r"__all_sync\([^;{]*moe_wait_h[^;{]*\{\s*__syncwarp\(\);", moe)

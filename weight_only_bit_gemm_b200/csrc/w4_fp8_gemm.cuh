@@ -143,6 +143,7 @@ struct Fp8Work {
 };
 
 __device__ __forceinline__ void epi_sync() {
+  __syncwarp();  // (the barrier is of whole warps)
   asm volatile("bar.sync 1, 256;" ::: "memory");
 }
 
@@ -375,7 +376,10 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       for (int kb = p.k0; kb < p.k1; ++kb, ++it) {
         const float f = f0;
         const uint32_t b = it & (C::kBufs - 1);
-        if (ok) ok = mbar_wait_warp(&tfull[b], (it / C::kBufs) & 1);
+        if (ok)
+          ok = mbar_wait_warp(&tfull[b], (it / C::kBufs) & 1);
+        else
+          __syncwarp();  // the tensor-memory loads are of whole warps
         tc_fence_after();
         if (busy) {
           // the next 16 columns load while the last are added
@@ -430,6 +434,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
               tma_store_3d(&ymap, yw, n0 + 64 * h, m0 + quad * 32, 0);
               bulk_commit();
             }
+            __syncwarp();
           } else {
             __syncwarp();
             for (int r = 0; r < 32 && quad * 32 + r < rows; ++r) {
@@ -550,7 +555,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   tc_fence_before();
   cluster_sync();  // neither CTA leaves while the other may reach its memory
   if (warp == 1) {
-    mbar_wait(done, 0);  // every issued MMA has completed
+    mbar_wait_warp(done, 0);  // every issued MMA has completed
     tc_fence_after();
     tmem_dealloc_pair(tmem, 512);
   }
@@ -768,7 +773,10 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks)
       }
       const float f = sc.f0;
       sc.shift();
-      if (ok) ok = mbar_wait_warp(&tfull[b], (i >> 1) & 1);
+      if (ok)
+        ok = mbar_wait_warp(&tfull[b], (i >> 1) & 1);
+      else
+        __syncwarp();  // the tensor-memory loads are of whole warps
       tc_fence_after();
       if (busy) {
         // the buffer goes back as soon as its columns are in registers: the
@@ -845,7 +853,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks)
   else
     __syncthreads();
   if (warp == C::kMma) {
-    mbar_wait(done, 0);  // every issued MMA has completed
+    mbar_wait_warp(done, 0);  // every issued MMA has completed
     tc_fence_after();
     tmem_dealloc(tmem, 256);
   }

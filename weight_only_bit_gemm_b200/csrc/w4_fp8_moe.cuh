@@ -374,7 +374,13 @@ __device__ __forceinline__ void moe_block_sums(const MoeArgs& a, const MoeBlocks
     const float f = UP ? sc.f0 : sc.f0 * w;
     sc.shift();
     --have;
-    if (ok) ok = mbar_wait_warp(&q.tfull[b], (i >> 1) & 1);
+    // (lanes whose token chose the expert have loaded scales, others have not;
+    // the tensor-memory loads are of whole warps)
+    if (!UP) __syncwarp();
+    if (ok)
+      ok = mbar_wait_warp(&q.tfull[b], (i >> 1) & 1);
+    else
+      __syncwarp();
     tc_fence_after();
     if (busy) {
       uint32_t v[2][16];
@@ -578,6 +584,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks)
       q.pb = a.s13 + (static_cast<size_t>(2 * expert + half) * a.IB + ib) * a.HB;
       moe_block_sums<true, C::kRow>(a, q, warp, lane);
     } else if (__all_sync(0xffffffffu, lane != 0 || moe_wait_h(a, h_want))) {
+      __syncwarp();  // (a vote alone orders no memory: lane 0 has seen h published)
       q.act = k0 / a.IB;
       q.k0 = k0 - q.act * a.IB;
       q.nt = nt;
@@ -679,7 +686,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks)
     }
   }
   if (warp == C::kMma) {
-    mbar_wait(done, 0);  // every issued MMA has completed
+    mbar_wait_warp(done, 0);  // every issued MMA has completed
     tc_fence_after();
     tmem_dealloc(tmem, 256);
   }

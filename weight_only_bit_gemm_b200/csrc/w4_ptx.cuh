@@ -97,9 +97,10 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity,
   }
 }
 
-// The same wait for a converged warp that waits often: a short loop without
-// branches on per-lane results, then the timed one.  Every lane gets the
-// answer of the whole warp.
+// The same wait for a whole warp that waits often: a short loop, then the timed
+// one.  Each lane leaves the loop by its own answer (try_wait promises no
+// common one), so the warp votes after it: every lane gets the answer of the
+// whole warp and the warp is converged again.
 __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -107,10 +108,10 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity) {
       "mov.u32 n, 64;\n\t"
       "W4_WAIT_%=:\n\t"
       "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "@p bra.uni W4_DONE_%=;\n\t"
+      "@p bra W4_DONE_%=;\n\t"
       "sub.u32 n, n, 1;\n\t"
       "setp.ne.u32 q, n, 0;\n\t"
-      "@q bra.uni W4_WAIT_%=;\n\t"
+      "@q bra W4_WAIT_%=;\n\t"
       "W4_DONE_%=:\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
@@ -164,8 +165,11 @@ __device__ __forceinline__ void mbar_arrive_cluster_lane0(uint32_t addr, int lan
       : "memory");
 }
 
-// Every thread of every CTA of the cluster: arrive, then wait for all.
+// Every thread of every CTA of the cluster: arrive, then wait for all.  The
+// barrier is of whole warps (.aligned), so lanes that took different ways to it
+// meet first.
 __device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
   asm volatile(
       "barrier.cluster.arrive.release.aligned;\n\t"
       "barrier.cluster.wait.acquire.aligned;" ::: "memory");
