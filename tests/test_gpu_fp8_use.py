@@ -1,0 +1,74 @@
+"""Ways of calling the block-scaled e4m3 path that a program may take: host
+threads that share a stream, tensors rewritten on the stream between calls,
+sizes and values at the ends of their ranges.  Results are compared with the
+same calls made alone, or with the oracle."""
+import threading
+
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_fp8 import dev, draw_moe, draw_x, ok, q_dev, x_dev
+from weight_only_bit_gemm_b200 import synthetic as S
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def w4():
+    from weight_only_bit_gemm_b200 import build
+    build.build()
+    from weight_only_bit_gemm_b200 import w4 as mod
+    return mod
+
+
+# ------------------------------------------------------------ host threads
+
+def in_threads(calls, turns):
+    """The results of each call, made `turns` times by a thread of its own, all
+    on the current stream."""
+    start, stream = threading.Barrier(len(calls)), torch.cuda.current_stream()
+    got = [[] for _ in calls]
+
+    def work(i):
+        with torch.cuda.stream(stream):
+            start.wait()
+            for _ in range(turns):
+                got[i].append(calls[i]())
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(calls))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert all(len(g) == turns for g in got)
+    return got
+
+
+def moe_tensors(data):
+    return tuple(conv(a) for conv, a in zip((x_dev, x_dev, q_dev, dev, q_dev, dev), data))
+
+
+def test_first_calls_of_a_host_thread(w4):
+    # a thread whose first call into CUDA is this library's: the tensor maps
+    # are made by driver calls, which need the device's context on the thread
+    qx, sx = w4.fp8_quantize_activations(x_dev(draw_x(200, 400, 1)))
+    qw, sw = w4.fp8_quantize_weights(dev(S.draw_w(300, 400, 0.02, seed=1, tag=90)))
+    moe = moe_tensors(draw_moe(2, 4, 256, 128, 62))
+    Wp = w4.prepack(*w4.quantize_rtn(dev(S.draw_w(256, 512, 0.02, seed=2, tag=90)), 128), 128)
+    X = x_dev(draw_x(300, 512, 2))
+    q1, s1 = qx[:3].contiguous(), sx[:3].contiguous()
+    y1, y200, y4 = (torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+                    for M, N in ((3, 300), (200, 300), (300, 256)))
+    ws = torch.zeros(64 << 20, dtype=torch.uint8, device="cuda")
+    calls = [lambda: w4.fp8_gemm(q1, s1, qw, sw, out=y1, workspace=ws).clone(),
+             lambda: w4.fp8_gemm(qx, sx, qw, sw, out=y200, workspace=ws).clone(),
+             lambda: w4.fp8_moe(*moe, 2, workspace=ws)[0],
+             lambda: w4.w4a16_gemm(X, Wp, 256, 512, 128, out=y4, workspace=ws).clone()]
+    for call in calls:
+        alone = call()
+        torch.cuda.synchronize()
+        (got,), = in_threads([call], 1)
+        assert torch.equal(got, alone)
+    ok(w4)
