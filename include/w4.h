@@ -497,8 +497,9 @@ w4_status fp8_add_rmsnorm(const uint16_t* X, const uint16_t* residual, const uin
  *              invalid or unsupported shape), 256-byte aligned, ZEROED ONCE before its first
  *              use; the call leaves its counters (the first 262144 bytes)
  *              zeroed, so calls of any shape, and w4a16_gemm / nf4_gemm, may
- *              share it as long as they are ordered on one stream.  After
- *              W4_ERR_TIMEOUT it must be zeroed again.
+ *              share it as long as they are ordered on one stream, from
+ *              whichever host threads.  After W4_ERR_TIMEOUT it must be
+ *              zeroed again.
  * As in w4a16_gemm the weights (qw, sw) are constant model state: they are
  * read before the kernel before this one on the stream has finished, and must
  * not be written by it (fp8_quantize_weights directly before is fine).      */

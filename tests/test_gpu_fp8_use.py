@@ -72,3 +72,23 @@ def test_first_calls_of_a_host_thread(w4):
         (got,), = in_threads([call], 1)
         assert torch.equal(got, alone)
     ok(w4)
+
+
+@pytest.mark.parametrize("own_workspace", [False, True])
+def test_two_host_threads_on_one_stream(w4, own_workspace):
+    # one stream and one workspace for both threads: the two kernels of an
+    # expert layer stay together, whatever the other thread's calls, of another
+    # shape, leave in the workspace between them
+    shapes = [(3, 8, 2, 512, 272), (40, 16, 4, 400, 144)]
+    kw = dict(workspace=torch.zeros(32 << 20, dtype=torch.uint8, device="cuda")) if own_workspace else {}
+    calls = []
+    for T, E, top, H, I in shapes:
+        a = moe_tensors(draw_moe(T, E, H, I, 60 + T))
+        calls.append(lambda a=a, top=top: w4.fp8_moe(*a, top, **kw))
+    alone = [c() for c in calls]
+    torch.cuda.synchronize()
+    got = in_threads(calls, 300)
+    ok(w4)
+    for g, e in zip(got, alone):
+        for r in g:
+            assert all(torch.equal(x, y) for x, y in zip(r, e))
