@@ -1,0 +1,64 @@
+"""The Python calls of the block-scaled e4m3 path around the library (no GPU
+needed: the library's entry points are stood in for, tensors are on the host)."""
+import gc
+import types
+import weakref
+
+import pytest
+import torch
+
+from weight_only_bit_gemm_b200 import build
+
+build.build()
+from weight_only_bit_gemm_b200 import w4  # noqa: E402
+
+F8 = torch.float8_e4m3fn
+STREAM = 7
+
+
+@pytest.fixture
+def host(monkeypatch):
+    """w4 with host tensors taken for a device's (index -1), a fake library and
+    no workspaces yet."""
+    monkeypatch.setattr(w4, "_fp8_first", lambda t, dtype, dim, name: -1)
+    monkeypatch.setattr(w4, "_raw_stream", lambda dev: STREAM)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    monkeypatch.setattr(w4, "_FP8_WS", {})
+    fake = types.SimpleNamespace(fp8_gemm_workspace_bytes=lambda *a: 1 << 21,
+                                 fp8_moe_workspace_bytes=lambda *a: 1 << 21)
+    monkeypatch.setattr(w4, "lib", fake)
+    return fake
+
+
+def gemm():
+    return w4.fp8_gemm(torch.zeros(4, 128).to(F8), torch.ones(4, 1), torch.zeros(8, 128).to(F8),
+                       torch.ones(1, 1))
+
+
+def moe():
+    return w4.fp8_moe(torch.zeros(1, 128, dtype=torch.bfloat16), torch.zeros(2, 128, dtype=torch.bfloat16),
+                      torch.zeros(2, 2, 128, 128).to(F8), torch.ones(2, 2, 1, 1),
+                      torch.zeros(2, 128, 128).to(F8), torch.ones(2, 1, 1), 1)
+
+
+@pytest.mark.parametrize("call,entry", [(gemm, "fp8_gemm"), (moe, "fp8_moe")])
+def test_workspace_outlives_its_replacement_by_another_thread(host, call, entry):
+    # while a call is on its way into the library, another thread's call needs a
+    # larger workspace of the same stream: the first one's must not be freed
+    # before its kernels are launched
+    seen = []
+
+    def launch(*args):
+        (key, buf), = w4._FP8_WS.items()
+        seen.append(weakref.ref(buf))
+        w4._FP8_WS[key] = torch.zeros(8, dtype=torch.uint8)
+        del buf
+        gc.collect()
+        assert seen[0]() is not None, "the workspace was freed before the launch"
+        return w4.W4_OK
+
+    setattr(host, entry, launch)
+    call()
+    assert len(seen) == 1
+    gc.collect()
+    assert seen[0]() is None            # nothing keeps it afterwards

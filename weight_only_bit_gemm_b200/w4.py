@@ -569,10 +569,12 @@ _FP8_COUNTER_BYTES = 65536 * 4
 
 
 def _fp8_workspace(need, workspace, like, dev, stream):
-    """(address, bytes) of the caller's workspace, or of one of this (device,
-    stream), zeroed when it is made.  A call that is being captured into a
-    graph gets its own, zeroed by the graph at each replay: graphs then share
-    none."""
+    """(address, bytes, tensor) of the caller's workspace, or of one of this
+    (device, stream), zeroed when it is made.  A call that is being captured
+    into a graph gets its own, zeroed by the graph at each replay: graphs then
+    share none.  The caller keeps the tensor until its kernels are launched:
+    another thread may put a larger one in its place meanwhile, and memory given
+    back before the launch could be handed to someone else ahead of it."""
     if workspace is not None:
         if workspace.dtype is not torch.uint8 or workspace.get_device() != dev or \
                 not workspace.is_contiguous():
@@ -589,7 +591,7 @@ def _fp8_workspace(need, workspace, like, dev, stream):
             _FP8_WS[dev, stream] = buf
     at = buf.data_ptr()
     skip = -at & 255
-    return at + skip, max(0, buf.numel() - skip)
+    return at + skip, max(0, buf.numel() - skip), buf
 
 
 def fp8_quantize_weights(W):
@@ -666,7 +668,7 @@ def fp8_gemm(qx, sx, qw, sw, out=None, workspace=None):
         raise W4Error(W4_ERR_UNSUPPORTED if valid else W4_ERR_INVALID_ARG,
                       "fp8_gemm_workspace_bytes")
     stream = _raw_stream(dev)
-    ws, ws_bytes = _fp8_workspace(need, workspace, qx, dev, stream)
+    ws, ws_bytes, _held = _fp8_workspace(need, workspace, qx, dev, stream)
     _check(lib.fp8_gemm(qx.data_ptr(), s1, w, s2, M, N, K, out.data_ptr(), ws, ws_bytes, stream),
            "fp8_gemm")
     return out
@@ -697,7 +699,7 @@ def fp8_moe(X, router, w13, s13, w2, s2, top_k, renormalize=True, out=None, work
     ids = torch.empty(T, top_k, dtype=torch.int32, device=X.device)
     weights = torch.empty(T, top_k, dtype=_F32, device=X.device)
     stream = _raw_stream(dev)
-    ws, ws_bytes = _fp8_workspace(need, workspace, X, dev, stream)
+    ws, ws_bytes, _held = _fp8_workspace(need, workspace, X, dev, stream)
     _check(lib.fp8_moe(X.data_ptr(), r, p13, q13, p2, q2, T, E, top_k, H, I,
                        1 if renormalize else 0, out.data_ptr(), ids.data_ptr(),
                        weights.data_ptr(), ws, ws_bytes, stream), "fp8_moe")
