@@ -62,3 +62,15 @@ def test_workspace_outlives_its_replacement_by_another_thread(host, call, entry)
     assert len(seen) == 1
     gc.collect()
     assert seen[0]() is None            # nothing keeps it afterwards
+
+
+@pytest.mark.parametrize("status", ["W4_ERR_TIMEOUT", "W4_ERR_BOUNDS", "W4_OK", "W4_ERR_DEVICE_INPUT"])
+def test_default_workspaces_given_up_after_a_call_that_did_not_run_through(host, monkeypatch, status):
+    # their counters may be nonzero, and no caller can reach them
+    monkeypatch.setattr(w4, "_stream", lambda: None)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    host.w4_device_status = lambda stream: getattr(w4, status)
+    w4._FP8_WS.update({(0, 5): torch.ones(8), (0, 6): torch.ones(8), (1, 5): torch.ones(8)})
+    assert w4.device_status() == getattr(w4, status)
+    lost = status in ("W4_ERR_TIMEOUT", "W4_ERR_BOUNDS")
+    assert sorted(w4._FP8_WS) == ([(1, 5)] if lost else [(0, 5), (0, 6), (1, 5)])

@@ -92,3 +92,21 @@ def test_two_host_threads_on_one_stream(w4, own_workspace):
     for g, e in zip(got, alone):
         for r in g:
             assert all(torch.equal(x, y) for x, y in zip(r, e))
+
+
+# ------------------------------------------------- after a wait that gave up
+
+def test_calls_after_a_timeout(w4):
+    # a wait has run out (the short one of the self-test): whatever the default
+    # workspaces' counters hold then, the next calls do not start from it
+    args = moe_tensors(draw_moe(5, 6, 400, 144, 63))
+    alone = w4.fp8_moe(*args, 2)
+    ok(w4)
+    here = (torch.cuda.current_device(), torch.cuda.current_stream().cuda_stream)
+    w4._FP8_WS[here].fill_(1)
+    w4.selftest_wait_timeout()
+    assert w4.device_status() == w4.W4_ERR_TIMEOUT
+    assert here not in w4._FP8_WS       # (else the next line must not run)
+    again = w4.fp8_moe(*args, 2)
+    ok(w4)
+    assert all(torch.equal(a, b) for a, b in zip(again, alone))

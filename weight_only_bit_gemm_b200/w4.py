@@ -160,8 +160,17 @@ def _cuda(t, dtype, name):
 
 
 def device_status() -> int:
-    """Synchronise the current stream and return/clear the device error word."""
-    return lib.w4_device_status(_stream())
+    """Synchronise the current stream and return/clear the device error word.
+    After a call that did not run through (W4_ERR_TIMEOUT, W4_ERR_BOUNDS) the
+    fp8 calls' default workspaces on this device, whose counters it may have
+    left nonzero, are given up: the next calls make new ones."""
+    status = lib.w4_device_status(_stream())
+    if status in (W4_ERR_TIMEOUT, W4_ERR_BOUNDS):
+        dev = torch.cuda.current_device()
+        for key in list(_FP8_WS):
+            if key[0] == dev:
+                _FP8_WS.pop(key, None)
+    return status
 
 
 def selftest_wait_timeout() -> None:
