@@ -8,7 +8,8 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_fp8 import dev, draw_moe, draw_x, ok, q_dev, x_dev
+import oracle as O
+from test_gpu_fp8 import codes, dev, draw_moe, draw_x, ok, q_dev, same_scales, x_dev
 from weight_only_bit_gemm_b200 import synthetic as S
 
 pytestmark = pytest.mark.gpu
@@ -110,3 +111,56 @@ def test_calls_after_a_timeout(w4):
     again = w4.fp8_moe(*args, 2)
     ok(w4)
     assert all(torch.equal(a, b) for a, b in zip(again, alone))
+
+
+# ------------------------------------------------------- the longest rows
+
+K_MAX = 2 ** 31 - 16                    # the largest K an int can name
+
+
+def tiled(dtype, M, K, seed):
+    """[M, K] of drawn values that repeat every 65536."""
+    x = torch.empty(M, K, dtype=dtype, device="cuda")
+    base = x_dev(draw_x(1, 65536, seed)).to(dtype).view(-1)
+    flat = x.view(-1)
+    n = flat.numel() // 65536
+    flat[: n * 65536].view(n, 65536).copy_(base)
+    flat[n * 65536:].copy_(base[: flat.numel() - n * 65536])
+    return x
+
+
+LAST = K_MAX // 128 * 128               # where a row's last, shorter block starts
+
+
+@pytest.mark.parametrize("at", [0, 2 ** 30, LAST - 128, LAST])
+def test_activation_rows_of_the_largest_length(w4, at, rows):
+    x, q, s = rows
+    qr, sr = O.fp8_quantize_rows(x[:, at:at + 128].float().cpu().numpy())
+    assert np.array_equal(codes(q[:, at:at + 128].contiguous()), qr)
+    same_scales(s[:, at // 128:at // 128 + 1].cpu().numpy(), sr)
+
+
+@pytest.fixture(scope="module")
+def rows(w4):
+    x = tiled(torch.bfloat16, 2, K_MAX, 64)
+    q, s = w4.fp8_quantize_activations(x)
+    ok(w4)
+    assert s.shape == (2, 2 ** 24)
+    return x, q, s
+
+
+@pytest.mark.parametrize("at", [0, 2 ** 30, LAST - 128, LAST])
+def test_weight_rows_of_the_largest_length(w4, at, weight_rows):
+    W, q, s = weight_rows
+    qr, sr = O.fp8_quantize_blocks(W[:, at:at + 128].cpu().numpy())
+    assert np.array_equal(codes(q[:, at:at + 128].contiguous()), qr)
+    same_scales(s[:, at // 128:at // 128 + 1].cpu().numpy(), sr)
+
+
+@pytest.fixture(scope="module")
+def weight_rows(w4):
+    W = tiled(torch.float32, 2, K_MAX, 65)
+    q, s = w4.fp8_quantize_weights(W)
+    ok(w4)
+    assert s.shape == (1, 2 ** 24)
+    return W, q, s

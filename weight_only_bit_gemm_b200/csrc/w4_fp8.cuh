@@ -43,6 +43,11 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   return d;
 }
 
+// Scales along n channels or rows, for any n of an int.
+__device__ __forceinline__ uint32_t fp8_blocks(int n) {
+  return (static_cast<uint32_t>(n) + (kFp8Block - 1)) / kFp8Block;
+}
+
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
 // 8 bf16 values of a 16-byte load, widened.
@@ -154,9 +159,9 @@ __global__ void __launch_bounds__(256) fp8_quantize_x_kernel(const uint16_t* X, 
       have[u] = b < blocks;
       at[u] = static_cast<size_t>(b) * kFp8Block + l * 8;
       if (RAGGED) {
-        const int kb_n = (K + kFp8Block - 1) / kFp8Block;
+        const uint32_t kb_n = fp8_blocks(K);
         const unsigned long long m = have[u] ? fast_div(static_cast<unsigned long long>(b), by_kb) : 0;
-        const int k = static_cast<int>(b - static_cast<long long>(m) * kb_n) * kFp8Block + l * 8;
+        const int k = static_cast<int>(b - static_cast<long long>(m * kb_n)) * kFp8Block + l * 8;
         have[u] = have[u] && k < K;
         at[u] = static_cast<size_t>(m) * K + k;
       }
@@ -185,7 +190,7 @@ __global__ void __launch_bounds__(kFp8WThreads, kFp8WBlocks) fp8_quantize_w_kern
                                                              uint8_t* q, float* s) {
   constexpr int kRows = kFp8WThreads / 16, kTurns = kFp8Block / kRows;
   __shared__ uint32_t wmax[kFp8WThreads / 32];
-  const uint32_t kb_n = (K + kFp8Block - 1) / kFp8Block, nb_n = (N + kFp8Block - 1) / kFp8Block;
+  const uint32_t kb_n = fp8_blocks(K), nb_n = fp8_blocks(N);
   const uint32_t bn = blockIdx.x / kb_n, kb = blockIdx.x - bn * kb_n;
   const uint32_t mat = bn / nb_n;
   const int nb = static_cast<int>(bn - mat * nb_n);
@@ -274,7 +279,7 @@ __global__ void __launch_bounds__(1024) fp8_add_rmsnorm_kernel(
   float total = 0.0f;
   for (int w = 0; w < warps; ++w) total += part[w];
   const float rstd = rsqrtf(total / static_cast<float>(K) + eps);
-  const int kb_n = (K + kFp8Block - 1) / kFp8Block;
+  const uint32_t kb_n = fp8_blocks(K);
 #pragma unroll
   for (int c = 0; c < CPT; ++c) {
     const int k = (static_cast<int>(threadIdx.x) + c * static_cast<int>(blockDim.x)) * 8;
