@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(1024) fp8_add_rmsnorm_kernel(
   float total = 0.0f;
   for (int w = 0; w < warps; ++w) total += part[w];
   const float rstd = rsqrtf(total / static_cast<float>(K) + eps);
-  const uint32_t kb_n = fp8_blocks(K);
+  const int kb_n = (K + kFp8Block - 1) / kFp8Block;  // K <= 65536
 #pragma unroll
   for (int c = 0; c < CPT; ++c) {
     const int k = (static_cast<int>(threadIdx.x) + c * static_cast<int>(blockDim.x)) * 8;
