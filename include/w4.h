@@ -500,9 +500,8 @@ w4_status fp8_add_rmsnorm(const uint16_t* X, const uint16_t* residual, const uin
  *              share it as long as they are ordered on one stream, from
  *              whichever host threads.  After W4_ERR_TIMEOUT it must be
  *              zeroed again.
- * As in w4a16_gemm the weights (qw, sw) are constant model state: they are
- * read before the kernel before this one on the stream has finished, and must
- * not be written by it (fp8_quantize_weights directly before is fine).      */
+ * Everything is read in the stream's order, the weights too (unlike Wp in
+ * w4a16_gemm): qw and sw may be written by any kernel ahead of the call.    */
 size_t fp8_gemm_workspace_bytes(int M, int N, int K);
 w4_status fp8_gemm(const uint8_t* qx, const float* sx, const uint8_t* qw, const float* sw, int M,
                    int N, int K, uint16_t* Y, void* workspace, size_t workspace_bytes,

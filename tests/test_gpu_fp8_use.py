@@ -164,3 +164,57 @@ def weight_rows(w4):
     ok(w4)
     assert s.shape == (1, 2 ** 24)
     return W, q, s
+
+
+# --------------------------------------- operands written on the stream before
+
+def ahead_of_the_gpu():
+    """A few milliseconds of work on the stream, so that the calls made next are
+    queued and follow each other on the GPU without a gap."""
+    a = torch.ones(8192, 8192, dtype=torch.bfloat16, device="cuda")
+    for _ in range(8):
+        a @ a
+
+
+def between(w4, how, small):
+    """What runs between the writer of an operand and the product."""
+    if how == "norm":                    # starts while the kernel ahead of it runs
+        w4.fp8_add_rmsnorm(*small)
+    elif how == "torch":
+        small[0].clone()
+
+
+@pytest.mark.parametrize("how", ["nothing", "norm", "torch"])
+@pytest.mark.parametrize("writer", ["quantizer", "copy"])
+@pytest.mark.parametrize("M", [3, 40, 300])
+def test_weights_written_on_the_stream(w4, M, writer, how):
+    # the product's weights are the codes of a kernel that may still run when
+    # the product's blocks are already on the SMs; in memory that held the turn
+    # before's codes
+    N, K = 16, 2048
+    X = [x_dev(draw_x(N, K, 70 + i)) for i in range(2)]
+    Q = [w4.fp8_quantize_activations(x)[0] for x in X]
+    qx, sx = w4.fp8_quantize_activations(x_dev(draw_x(M, K, 72)))
+    sw = torch.full((1, K // 128), 2.0 ** -6, device="cuda")
+    small = (x_dev(draw_x(2, 256, 73)), torch.ones(256, dtype=torch.bfloat16, device="cuda"))
+    alone = []
+    for q in Q:
+        torch.cuda.synchronize()
+        alone.append(w4.fp8_gemm(qx, sx, q, sw))
+    torch.cuda.synchronize()
+    assert not torch.equal(*alone)
+    held, scales, got = torch.empty_like(Q[0]), torch.empty(N, K // 128, device="cuda"), []
+    ahead_of_the_gpu()
+    for turn in range(100):
+        i = turn & 1
+        if writer == "quantizer":
+            w4._check(w4.lib.fp8_quantize_activations(X[i].data_ptr(), N, K, held.data_ptr(),
+                                                      scales.data_ptr(), w4._raw_stream(0)), "quantize")
+        else:
+            held.copy_(Q[i])
+        between(w4, how, small)
+        got.append(w4.fp8_gemm(qx, sx, held, sw))
+    torch.cuda.synchronize()
+    ok(w4)
+    bad = [t for t, y in enumerate(got) if not torch.equal(y, alone[t & 1])]
+    assert not bad, f"{len(bad)} of {len(got)} turns saw other weights"

@@ -232,8 +232,6 @@ __global__ void __launch_bounds__(kFp8WThreads, kFp8WBlocks) fp8_quantize_w_kern
       *reinterpret_cast<uint2*>(qm + static_cast<size_t>(n) * K + k) = fp8_codes8_neg(u, sc);
   }
   if (threadIdx.x == 0) s[blockIdx.x] = sc;
-  // a product launched next may read the weights before this grid has ended
-  __threadfence();
 }
 
 // ---------------------------------------------------------------- RMS norm

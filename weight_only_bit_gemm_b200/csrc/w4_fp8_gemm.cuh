@@ -212,9 +212,9 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       auto arm = [&](int s) {  // a pair: the leader's barrier counts both CTAs' bytes
         if (rank == 0) mbar_arrive_expect_tx(&full[s], kBytes);
       };
+      auto w_row = [&](int nt) { return nt * C::NT + static_cast<int>(rank) * C::kWRows; };
       auto load_w = [&](int s, int nt, int kb) {
-        tma_load_3d_pair(ws + s * C::kWStage, &wmap, kb * 128,
-                         nt * C::NT + static_cast<int>(rank) * C::kWRows, 0,
+        tma_load_3d_pair(ws + s * C::kWStage, &wmap, kb * 128, w_row(nt), 0,
                          mapa_shared(smem_u32(&full[s]), 0), pol_w);
       };
       auto load_x = [&](int s, int mt, int kb) {
@@ -222,18 +222,17 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         tma_load_3d_pair(xs + s * C::kXStage, &xmap, kb * 128, m, 0,
                          mapa_shared(smem_u32(&full[s]), 0), pol_x);
       };
-      // the weights do not depend on the previous kernel: the first ring of
-      // them is requested before the dependency wait
-      int early = 0;
+      // before the dependency wait the first ring of weights is on its way into
+      // L2; they are read after it, like everything that a kernel ahead on the
+      // stream may have written
       {
         Fp8Work w2 = work;
+        int early = 0;
         while (early < C::STAGES && w2.next(p)) {
           int mt, nt;
           w2.tile_at(p.tile, mt, nt);
-          for (int kb = p.k0; kb < p.k1 && early < C::STAGES; ++kb, ++early) {
-            arm(early);
-            load_w(early, nt, kb);
-          }
+          for (int kb = p.k0; kb < p.k1 && early < C::STAGES; ++kb, ++early)
+            tma_prefetch_3d(&wmap, kb * 128, w_row(nt), 0, pol_w);
         }
       }
       grid_dep_wait();
@@ -244,14 +243,12 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         work.tile_at(p.tile, mt, nt);
         for (int kb = p.k0; kb < p.k1; ++kb, ++it) {
           const int s = it % C::STAGES;
-          if (it >= C::STAGES) {
-            if (!mbar_wait(&empty[s], ((it / C::STAGES) - 1) & 1)) {
-              ok = false;
-              break;
-            }
-            arm(s);
-            load_w(s, nt, kb);
+          if (it >= C::STAGES && !mbar_wait(&empty[s], ((it / C::STAGES) - 1) & 1)) {
+            ok = false;
+            break;
           }
+          arm(s);
+          load_w(s, nt, kb);
           load_x(s, mt, kb);
         }
       }
@@ -686,20 +683,19 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks)
       const uint64_t pol_w = policy_evict_first();  // read once
       const uint64_t pol_x = policy_evict_last();
       const uint32_t bytes = C::kWStage + static_cast<uint32_t>(a.M) * 128u;
-      // the weights do not depend on the previous kernel
-      for (int i = 0; i < n && i < C::STAGES; ++i) {
-        mbar_arrive_expect_tx(&full[i], bytes);
-        tma_load_3d(ws + i * C::kWStage, &wmap, (k0 + i) * 128, nt * 128, 0, &full[i], pol_w);
-      }
+      // the first ring of weights into L2 ahead of the dependency wait, as in the
+      // pair kernel (1 x 4096 x 4096 in a chain of products 7.3 us, without it
+      // 7.7; four rings 7.7, they displace each other.  Weights read ahead of
+      // the wait, out of the stream's order, were 6.8)
+      for (int i = 0; i < n && i < C::STAGES; ++i)
+        tma_prefetch_3d(&wmap, (k0 + i) * 128, nt * 128, 0, pol_w);
       grid_dep_wait();
       int i = 0;
       for (; i < n; ++i) {
         const int s = i % C::STAGES;
-        if (i >= C::STAGES) {
-          if (!mbar_wait(&empty[s], ((i / C::STAGES) - 1) & 1)) break;
-          mbar_arrive_expect_tx(&full[s], bytes);
-          tma_load_3d(ws + s * C::kWStage, &wmap, (k0 + i) * 128, nt * 128, 0, &full[s], pol_w);
-        }
+        if (i >= C::STAGES && !mbar_wait(&empty[s], ((i / C::STAGES) - 1) & 1)) break;
+        mbar_arrive_expect_tx(&full[s], bytes);
+        tma_load_3d(ws + s * C::kWStage, &wmap, (k0 + i) * 128, nt * 128, 0, &full[s], pol_w);
         tma_load_3d(xs + s * C::kXStage, &xmap, (k0 + i) * 128, 0, 0, &full[s], pol_x);
       }
       // never leave with copies in flight

@@ -216,7 +216,19 @@ __device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* m
       : "memory");
 }
 
-// The same for a CTA pair (cta_group::2): the tile lands in this CTA's shared
+// The same box into L2 only.  Nothing is read by it (L2 is where every SM's
+// writes meet, so a later write reaches the line): it may run ahead of the
+// kernel that writes the box.
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int c0, int c1, int c2,
+                                                uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.prefetch.tensor.3d.L2.global.tile.L2::cache_hint [%0, {%1, %2, %3}], %4;" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(c0), "r"(c1), "r"(c2), "l"(policy)
+      : "memory");
+}
+
+// The same as tma_load_3d for a CTA pair (cta_group::2): the tile lands in this CTA's shared
 // memory and its bytes are counted on the mbarrier at `bar_cluster` (a
 // shared::cluster address, here the pair's leader's).  No multicast.
 __device__ __forceinline__ void tma_load_3d_pair(void* smem_dst, const CUtensorMap* map, int c0,

@@ -660,9 +660,7 @@ def fp8_add_rmsnorm(X, weight, residual=None, eps=1e-6, want_y=False, residual_o
 
 def fp8_gemm(qx, sx, qw, sw, out=None, workspace=None):
     """bf16 Y[M, N] = (qx sx) . (qw sw)^T for codes and scales as
-    fp8_quantize_activations / fp8_add_rmsnorm and fp8_quantize_weights give them.
-    The weights are constant model state: another library's kernel that writes
-    them must have finished before this call (see w4.h)."""
+    fp8_quantize_activations / fp8_add_rmsnorm and fp8_quantize_weights give them."""
     dev = _fp8_first(qx, _E4M3, 2, "qx")
     M, K = qx.shape
     N = qw.shape[0]
