@@ -45,3 +45,12 @@ def test_warps_are_whole_at_their_barriers():
     # a vote orders no memory: the lanes that did not wait for h themselves
     moe = source("w4_fp8_moe.cuh")
     assert re.search(r"__all_sync\([^;{]*moe_wait_h[^;{]*\{\s*__syncwarp\(\);", moe)
+
+
+@pytest.mark.parametrize("name", ["w4_fp8.cuh", "w4_fp8_gemm.cuh", "w4_fp8_moe.cuh"])
+def test_no_read_only_loads_of_what_a_kernel_ahead_may_write(name):
+    # these kernels are resident while the kernel ahead of them runs: a load
+    # declared read-only for the kernel's life (ld.global.nc) may be moved ahead
+    # of the dependency wait or meet an old line in L1
+    text = source(name)
+    assert "__ldg(" not in text and "ld.global.nc" not in text and "__restrict__" not in text

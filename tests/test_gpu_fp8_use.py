@@ -218,3 +218,56 @@ def test_weights_written_on_the_stream(w4, M, writer, how):
     ok(w4)
     bad = [t for t, y in enumerate(got) if not torch.equal(y, alone[t & 1])]
     assert not bad, f"{len(bad)} of {len(got)} turns saw other weights"
+
+
+@pytest.mark.parametrize("M", [3, 200])
+def test_weight_scales_written_on_the_stream(w4, M):
+    # an SM may still hold the lines of the product before, which read the same
+    # memory's older scales while this product's blocks were already resident
+    K, NB = 512, 296                    # two blocks on every SM
+    N = NB * 128
+    X = [x_dev(draw_x(NB, K, 80 + i)) for i in range(2)]
+    qx, sx = w4.fp8_quantize_activations(x_dev(draw_x(M, K, 82)))
+    qw, _ = w4.fp8_quantize_weights(dev(S.draw_w(N, K, 0.02, seed=4, tag=91)))
+    S2 = [w4.fp8_quantize_activations(x)[1] for x in X]
+    alone = [w4.fp8_gemm(qx, sx, qw, s) for s in S2]
+    torch.cuda.synchronize()
+    assert not torch.equal(*alone)
+    q, s, got = torch.empty(NB, K, dtype=torch.uint8, device="cuda"), torch.empty_like(S2[0]), []
+    ahead_of_the_gpu()
+    for turn in range(400):
+        w4._check(w4.lib.fp8_quantize_activations(X[turn & 1].data_ptr(), NB, K, q.data_ptr(), s.data_ptr(),
+                                                  w4._raw_stream(0)), "quantize")
+        got.append(w4.fp8_gemm(qx, sx, qw, s))
+    torch.cuda.synchronize()
+    ok(w4)
+    assert [t for t, y in enumerate(got) if not torch.equal(y, alone[t & 1])] == []
+
+
+@pytest.mark.parametrize("call", ["norm", "norm of many rows", "moe"])
+def test_vectors_written_on_the_stream(w4, call):
+    # the norm's weight and the router, written by a product on the stream
+    K, E = 4096, 8
+    qx, sx = zip(*(w4.fp8_quantize_activations(x_dev(draw_x(E, K, 84 + i))) for i in range(2)))
+    qw, sw = w4.fp8_quantize_weights(dev(S.draw_w(K, K, 0.02, seed=3, tag=91)))
+    x = x_dev(draw_x(700 if "many" in call else 2, K, 86))
+    moe = moe_tensors(draw_moe(2, E, K, 128, 87))
+    vec = [w4.fp8_gemm(a, b, qw, sw) for a, b in zip(qx, sx)]
+
+    def use(v):
+        if call == "moe":
+            return w4.fp8_moe(x, v, *moe[2:], 2)[2]
+        return w4.fp8_add_rmsnorm(x, v[0], want_y=True)[3]
+
+    alone = [use(v) for v in vec]
+    torch.cuda.synchronize()
+    assert not torch.equal(*alone)
+    held, got = torch.empty_like(vec[0]), []
+    ahead_of_the_gpu()
+    for turn in range(200):
+        i = turn & 1
+        w4.fp8_gemm(qx[i], sx[i], qw, sw, out=held)
+        got.append(use(held))
+    torch.cuda.synchronize()
+    ok(w4)
+    assert [t for t, y in enumerate(got) if not torch.equal(y, alone[t & 1])] == []

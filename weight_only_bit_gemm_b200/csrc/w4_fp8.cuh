@@ -14,8 +14,10 @@
 //
 // The kernels start before the kernel ahead of them on the stream has ended
 // (programmatic dependent launch).  What that kernel may write is read after
-// the dependency wait and from L2 (ld.cg): this SM's L1 can still hold lines
-// that the kernel before it read while this one was already resident.
+// the dependency wait and from L2 (ld.cg), every operand: this SM's L1 can still
+// hold lines that the kernel before it read while this one was already
+// resident, and a load declared read-only (ld.global.nc) may be moved ahead of
+// the wait.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -244,7 +246,7 @@ __global__ void __launch_bounds__(kFp8WThreads, kFp8WBlocks) fp8_quantize_w_kern
 // us, 6.2 TB/s; one row of 4096 in 2.4 us, the launch.
 template <int CPT>
 __global__ void __launch_bounds__(1024) fp8_add_rmsnorm_kernel(
-    const uint16_t* x, const uint16_t* residual, const uint16_t* __restrict__ weight, float eps,
+    const uint16_t* x, const uint16_t* residual, const uint16_t* weight, float eps,
     int K, uint16_t* residual_out, uint16_t* y_out, uint8_t* q, float* s) {
   __shared__ float part[32];
   grid_dep_launch();
@@ -293,7 +295,7 @@ __global__ void __launch_bounds__(1024) fp8_add_rmsnorm_kernel(
       *reinterpret_cast<uint4*>(residual_out + row + k) = o;
     }
     float w8[8] = {};
-    if (have) unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(weight + k)), w8);
+    if (have) unpack_bf16x8(__ldcg(reinterpret_cast<const uint4*>(weight + k)), w8);
     uint32_t mx = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {

@@ -327,11 +327,11 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     auto scales = [&](int g) {
       if (a.vec_s) {
         sx4 = __ldcg(reinterpret_cast<const float4*>(sxp + g));
-        sw4 = __ldg(reinterpret_cast<const float4*>(swp + g));
+        sw4 = __ldcg(reinterpret_cast<const float4*>(swp + g));
       } else {
         const int g1 = min(g + 1, a.KB - 1), g2 = min(g + 2, a.KB - 1), g3 = min(g + 3, a.KB - 1);
         sx4 = make_float4(__ldcg(sxp + g), __ldcg(sxp + g1), __ldcg(sxp + g2), __ldcg(sxp + g3));
-        sw4 = make_float4(__ldg(swp + g), __ldg(swp + g1), __ldg(swp + g2), __ldg(swp + g3));
+        sw4 = make_float4(__ldcg(swp + g), __ldcg(swp + g1), __ldcg(swp + g2), __ldcg(swp + g3));
       }
     };
     auto begin = [&](const Fp8Piece& q) {
@@ -595,7 +595,7 @@ struct Fp8Scales {
   float4 x, w;  // the next group, as loaded
   __device__ __forceinline__ void load4(const float* px, const float* pw) {
     x = __ldcg(reinterpret_cast<const float4*>(px));
-    w = __ldg(reinterpret_cast<const float4*>(pw));
+    w = __ldcg(reinterpret_cast<const float4*>(pw));
   }
   __device__ __forceinline__ void take() {
     f0 = x.x * w.x;
@@ -752,7 +752,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks)
       } else {
         const int i1 = min(i + 1, n - 1), i2 = min(i + 2, n - 1), i3 = min(i + 3, n - 1);
         sc.x = make_float4(__ldcg(sxp + i), __ldcg(sxp + i1), __ldcg(sxp + i2), __ldcg(sxp + i3));
-        sc.w = make_float4(__ldg(swp + i), __ldg(swp + i1), __ldg(swp + i2), __ldg(swp + i3));
+        sc.w = make_float4(__ldcg(swp + i), __ldcg(swp + i1), __ldcg(swp + i2), __ldcg(swp + i3));
       }
     };
     grid_dep_wait();

@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(256) moe_route_kernel(const MoeArgs a) {
       uint4 rw[8];
 #pragma unroll
       for (int c = 0; c < 8; ++c)
-        rw[c] = k + c * 256 < a.H ? __ldg(reinterpret_cast<const uint4*>(r + k + c * 256))
+        rw[c] = k + c * 256 < a.H ? __ldcg(reinterpret_cast<const uint4*>(r + k + c * 256))
                                   : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
       for (int i = 0; i < kMoeRouteTokens; ++i) {
@@ -350,7 +350,7 @@ __device__ __forceinline__ void moe_block_sums(const MoeArgs& a, const MoeBlocks
     } else {
       const int k1 = min(kb + 1, len - 1), k2 = min(kb + 2, len - 1), k3 = min(kb + 3, len - 1);
       sc.x = make_float4(__ldcg(pa + kb), __ldcg(pa + k1), __ldcg(pa + k2), __ldcg(pa + k3));
-      sc.w = make_float4(__ldg(pb + kb), __ldg(pb + k1), __ldg(pb + k2), __ldg(pb + k3));
+      sc.w = make_float4(__ldcg(pb + kb), __ldcg(pb + k1), __ldcg(pb + k2), __ldcg(pb + k3));
     }
     kb += have_req;
     left -= have_req;
