@@ -54,3 +54,28 @@ def test_no_read_only_loads_of_what_a_kernel_ahead_may_write(name):
     # of the dependency wait or meet an old line in L1
     text = source(name)
     assert "__ldg(" not in text and "ld.global.nc" not in text and "__restrict__" not in text
+
+
+# loads whose index is a loop's own (below the bound in the loop's condition) or
+# checked on the lines before
+LOOP_LOADS = ("a.ids + i", "a.weights + i", "a.active)", "src + (2 * c8 + h) * kFp8Rows + r", "p)", "p + 1)")
+
+
+@pytest.mark.parametrize("name", ["w4_fp8.cuh", "w4_fp8_gemm.cuh", "w4_fp8_moe.cuh"])
+def test_global_accesses_go_through_the_bounds_checks(name):
+    # the bounds-checked build can only report an access that asks it
+    text = source(name)
+    if name == "w4_fp8.cuh":
+        for head in (r"\bV ld_in\(", r"\bvoid st_in\("):
+            part = body(text, head)
+            assert "in_bounds(" in part
+            text = text.replace(part, "{}")
+    loads = re.findall(r"__ldc[gs]\(([^;]*)", text)
+    assert all(l.startswith(LOOP_LOADS) for l in loads), loads
+    # vector stores that are left go to shared memory
+    for target in re.findall(r"\*reinterpret_cast<u?int\w*\*>\((\w+)", text):
+        assert target == "yw", target
+    # scalar stores through an operand's pointer: the loop's own index
+    for operand in re.findall(r"\b(?:a\.)?(Y|y|q|qm|y_out|residual_out|logits|ids|weights|xq|sx|wt|hq|sh)"
+                              r"\[[^\]]*\] = ", text):
+        raise AssertionError(operand)

@@ -31,6 +31,19 @@ namespace w4 {
 constexpr int kFp8Block = 128;       // channels (and weight rows) per scale
 constexpr float kFp8Max = 448.0f;    // largest e4m3 value
 
+// A vector V at p, somewhere in an array of n elements from base: read from L2
+// (zero where the bounds-checked build finds it outside), or written.
+template <class V, class T>
+__device__ __forceinline__ V ld_in(const T* p, const T* base, unsigned long long n) {
+  if (!in_bounds(static_cast<unsigned long long>(p - base) + sizeof(V) / sizeof(T) - 1, n)) return V{};
+  return __ldcg(reinterpret_cast<const V*>(p));
+}
+template <class T, class V>
+__device__ __forceinline__ void st_in(T* p, const T* base, unsigned long long n, V v) {
+  if (in_bounds(static_cast<unsigned long long>(p - base) + sizeof(V) / sizeof(T) - 1, n))
+    *reinterpret_cast<V*>(p) = v;
+}
+
 // The scale of a block whose largest |v| has these bits.
 __device__ __forceinline__ float fp8_scale(uint32_t max_bits) {
   if (max_bits >= 0x7F800000u) return __uint_as_float(0x7FC00000u);
@@ -143,9 +156,9 @@ __device__ __forceinline__ uint32_t abs_max_bf16x8(uint4 w) {
 // 40 us, 4.3 TB/s (with one-wide fp32 arithmetic and U = 2 45 us, U = 1 53 us,
 // U = 4 58 us).
 template <int U, bool RAGGED>
-__global__ void __launch_bounds__(256) fp8_quantize_x_kernel(const uint16_t* X, long long blocks,
-                                                             int K, FastDivIdx by_kb, uint8_t* q,
-                                                             float* s) {
+__global__ void __launch_bounds__(256)
+    fp8_quantize_x_kernel(const uint16_t* X, long long blocks, int K, FastDivIdx by_kb, uint8_t* q,
+                          float* s, unsigned long long values) {  // M K
   grid_dep_launch();
   grid_dep_wait();
   const int l = threadIdx.x & 15;
@@ -167,14 +180,14 @@ __global__ void __launch_bounds__(256) fp8_quantize_x_kernel(const uint16_t* X, 
         have[u] = have[u] && k < K;
         at[u] = static_cast<size_t>(m) * K + k;
       }
-      w[u] = have[u] ? __ldcg(reinterpret_cast<const uint4*>(X + at[u])) : make_uint4(0u, 0u, 0u, 0u);
+      w[u] = have[u] ? ld_in<uint4>(X + at[u], X, values) : make_uint4(0u, 0u, 0u, 0u);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       float v[8];  // negated
       unpack_neg_bf16x8(w[u], v);
       const float sc = fp8_scale(half_warp_max(abs_max_bf16x8(w[u])));
-      if (have[u]) *reinterpret_cast<uint2*>(q + at[u]) = fp8_codes8_neg(v, sc);
+      if (have[u]) st_in(q + at[u], q, values, fp8_codes8_neg(v, sc));
       const long long b = b0 + u * step + threadIdx.x / 16;
       if (l == 0 && b < blocks) s[b] = sc;
     }
@@ -188,8 +201,9 @@ constexpr int kFp8WThreads = 256, kFp8WBlocks = 3;
 // channels per lane, 16 rows at a time; the values stay in registers between
 // the maximum and the codes.  Bound by HBM: 16 x 2000 x 4096 in 115 us, 5.7 TB/s
 // (2 CTAs per SM 126 us; CTAs of 512 threads, 2 per SM, 119 us).
-__global__ void __launch_bounds__(kFp8WThreads, kFp8WBlocks) fp8_quantize_w_kernel(const float* W, int N, int K,
-                                                             uint8_t* q, float* s) {
+__global__ void __launch_bounds__(kFp8WThreads, kFp8WBlocks)
+    fp8_quantize_w_kernel(const float* W, int N, int K, uint8_t* q, float* s,
+                          unsigned long long values) {  // B N K
   constexpr int kRows = kFp8WThreads / 16, kTurns = kFp8Block / kRows;
   __shared__ uint32_t wmax[kFp8WThreads / 32];
   const uint32_t kb_n = fp8_blocks(K), nb_n = fp8_blocks(N);
@@ -205,7 +219,8 @@ __global__ void __launch_bounds__(kFp8WThreads, kFp8WBlocks) fp8_quantize_w_kern
   for (int i = 0; i < kTurns; ++i) {
     const int n = nb * kFp8Block + r0 + kRows * i;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-    if (n < N && k < K) {
+    if (n < N && k < K &&
+        in_bounds(static_cast<unsigned long long>(Wm - W) + static_cast<size_t>(n) * K + k + 7, values)) {
       const float4* p = reinterpret_cast<const float4*>(Wm + static_cast<size_t>(n) * K + k);
       a = __ldcs(p);
       b = __ldcs(p + 1);
@@ -230,8 +245,7 @@ __global__ void __launch_bounds__(kFp8WThreads, kFp8WBlocks) fp8_quantize_w_kern
     float u[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) u[j] = -v[i][j];
-    if (n < N && k < K)
-      *reinterpret_cast<uint2*>(qm + static_cast<size_t>(n) * K + k) = fp8_codes8_neg(u, sc);
+    if (n < N && k < K) st_in(qm + static_cast<size_t>(n) * K + k, q, values, fp8_codes8_neg(u, sc));
   }
   if (threadIdx.x == 0) s[blockIdx.x] = sc;
 }
@@ -244,14 +258,18 @@ __global__ void __launch_bounds__(kFp8WThreads, kFp8WBlocks) fp8_quantize_w_kern
 // Every thread reads its own channels before it writes them, so residual_out
 // may be residual or x.  Bound by HBM: 8191 x 8192 with every output in 97
 // us, 6.2 TB/s; one row of 4096 in 2.4 us, the launch.
+// Up to 16384 channels a thread has 32 registers, which fills an SM with threads;
+// left to itself the compiler's choice moves with small changes (50 registers:
+// 8191 x 8192 in 129 us).
 template <int CPT>
-__global__ void __launch_bounds__(1024) fp8_add_rmsnorm_kernel(
+__global__ void __launch_bounds__(1024, CPT <= 2 ? 2 : 1) fp8_add_rmsnorm_kernel(
     const uint16_t* x, const uint16_t* residual, const uint16_t* weight, float eps,
     int K, uint16_t* residual_out, uint16_t* y_out, uint8_t* q, float* s) {
   __shared__ float part[32];
   grid_dep_launch();
   grid_dep_wait();
   const size_t row = static_cast<size_t>(blockIdx.x) * K;
+  const unsigned long long values = static_cast<unsigned long long>(gridDim.x) * K;
   float v[CPT][8];
   float ss = 0.0f;
 #pragma unroll
@@ -260,10 +278,10 @@ __global__ void __launch_bounds__(1024) fp8_add_rmsnorm_kernel(
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[c][j] = 0.0f;
     if (k < K) {
-      unpack_bf16x8(__ldcg(reinterpret_cast<const uint4*>(x + row + k)), v[c]);
+      unpack_bf16x8(ld_in<uint4>(x + row + k, x, values), v[c]);
       if (residual) {
         float r[8];
-        unpack_bf16x8(__ldcg(reinterpret_cast<const uint4*>(residual + row + k)), r);
+        unpack_bf16x8(ld_in<uint4>(residual + row + k, residual, values), r);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[c][j] += r[j];
       }
@@ -292,10 +310,10 @@ __global__ void __launch_bounds__(1024) fp8_add_rmsnorm_kernel(
         p[j] = static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(v[c][2 * j]))) |
                (static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(v[c][2 * j + 1]))) << 16);
       o.x = p[0]; o.y = p[1]; o.z = p[2]; o.w = p[3];
-      *reinterpret_cast<uint4*>(residual_out + row + k) = o;
+      st_in(residual_out + row + k, residual_out, values, o);
     }
     float w8[8] = {};
-    if (have) unpack_bf16x8(__ldcg(reinterpret_cast<const uint4*>(weight + k)), w8);
+    if (have) unpack_bf16x8(ld_in<uint4>(weight + k, weight, K), w8);
     uint32_t mx = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -312,10 +330,11 @@ __global__ void __launch_bounds__(1024) fp8_add_rmsnorm_kernel(
       for (int j = 0; j < 4; ++j)
         p[j] = static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(-v[c][2 * j]))) |
                (static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(-v[c][2 * j + 1]))) << 16);
-      *reinterpret_cast<uint4*>(y_out + row + k) = make_uint4(p[0], p[1], p[2], p[3]);
+      st_in(y_out + row + k, y_out, values, make_uint4(p[0], p[1], p[2], p[3]));
     }
-    *reinterpret_cast<uint2*>(q + row + k) = fp8_codes8_neg(v[c], sc);
-    if ((threadIdx.x & 15) == 0) s[static_cast<size_t>(blockIdx.x) * kb_n + k / kFp8Block] = sc;
+    st_in(q + row + k, q, values, fp8_codes8_neg(v[c], sc));
+    if ((threadIdx.x & 15) == 0 && in_bounds(k / kFp8Block, kb_n))
+      s[static_cast<size_t>(blockIdx.x) * kb_n + k / kFp8Block] = sc;
   }
 }
 

@@ -324,14 +324,20 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     const float *sxp = nullptr, *swp = nullptr;
     int mt = 0, nt = 0;
     float4 sx4, sw4;  // of the next group of four
+    const auto x1 = [&](int g) {
+      return ld_in<float>(sxp + g, a.sx, static_cast<unsigned long long>(a.M) * a.KB);
+    };
+    const auto w1 = [&](int g) {
+      return ld_in<float>(swp + g, a.sw, static_cast<unsigned long long>(a.NB) * a.KB);
+    };
     auto scales = [&](int g) {
       if (a.vec_s) {
-        sx4 = __ldcg(reinterpret_cast<const float4*>(sxp + g));
-        sw4 = __ldcg(reinterpret_cast<const float4*>(swp + g));
+        sx4 = ld_in<float4>(sxp + g, a.sx, static_cast<unsigned long long>(a.M) * a.KB);
+        sw4 = ld_in<float4>(swp + g, a.sw, static_cast<unsigned long long>(a.NB) * a.KB);
       } else {
         const int g1 = min(g + 1, a.KB - 1), g2 = min(g + 2, a.KB - 1), g3 = min(g + 3, a.KB - 1);
-        sx4 = make_float4(__ldcg(sxp + g), __ldcg(sxp + g1), __ldcg(sxp + g2), __ldcg(sxp + g3));
-        sw4 = make_float4(__ldcg(swp + g), __ldcg(swp + g1), __ldcg(swp + g2), __ldcg(swp + g3));
+        sx4 = make_float4(x1(g), x1(g1), x1(g2), x1(g3));
+        sw4 = make_float4(w1(g), w1(g1), w1(g2), w1(g3));
       }
     };
     auto begin = [&](const Fp8Piece& q) {
@@ -440,8 +446,9 @@ __global__ void __launch_bounds__(C::kThreads, 1)
               for (int c = 0; c < 2; ++c) {
                 const int col = 32 * c + lane;
                 if (n0 + 64 * h + col < a.N)
-                  y[col] = *reinterpret_cast<const uint16_t*>(yw + r * 128 +
-                                                              (((col >> 3) ^ (r & 7)) << 4) + (col & 7) * 2);
+                  st_in(y + col, a.Y, static_cast<unsigned long long>(a.M) * a.N,
+                        *reinterpret_cast<const uint16_t*>(yw + r * 128 + (((col >> 3) ^ (r & 7)) << 4) +
+                                                           (col & 7) * 2));
               }
             }
             __syncwarp();
@@ -470,12 +477,14 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       }
       epi_sync();
       if (threadIdx.x == 128) {
-        unsigned int* ctr = a.counter + tt * 2 + static_cast<int>(rank);
-        // (the barrier and this acquire-release publish the CTA's sums and make
-        // the other runs' visible)
-        const unsigned prev = atom_add_acq_rel_gpu(ctr, 1u);
-        const bool is_last = prev == static_cast<unsigned>(last - first);
-        if (is_last) *ctr = 0u;  // leave the workspace zeroed
+        bool is_last = false;
+        if (in_bounds(static_cast<unsigned>(tt), a.tail)) {
+          unsigned int* ctr = a.counter + tt * 2 + static_cast<int>(rank);
+          // (the barrier and this acquire-release publish the CTA's sums and make
+          // the other runs' visible)
+          is_last = atom_add_acq_rel_gpu(ctr, 1u) == static_cast<unsigned>(last - first);
+          if (is_last) *ctr = 0u;  // leave the workspace zeroed
+        }
         *last_flag = is_last ? 1 : 0;
       }
       epi_sync();
@@ -535,12 +544,15 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             const float o[8] = {sum[j][0].x, sum[j][0].y, sum[j][0].z, sum[j][0].w,
                                 sum[j][1].x, sum[j][1].y, sum[j][1].z, sum[j][1].w};
             if (a.vec && n + 8 <= a.N) {
-              *reinterpret_cast<uint4*>(y) = make_uint4(bf16_pack2(o[0], o[1]), bf16_pack2(o[2], o[3]),
-                                                        bf16_pack2(o[4], o[5]), bf16_pack2(o[6], o[7]));
+              st_in(y, a.Y, static_cast<unsigned long long>(a.M) * a.N,
+                    make_uint4(bf16_pack2(o[0], o[1]), bf16_pack2(o[2], o[3]), bf16_pack2(o[4], o[5]),
+                               bf16_pack2(o[6], o[7])));
             } else {
 #pragma unroll
               for (int i = 0; i < 8; ++i)
-                if (n + i < a.N) y[i] = __bfloat16_as_ushort(__float2bfloat16_rn(o[i]));
+                if (n + i < a.N)
+                  st_in(y + i, a.Y, static_cast<unsigned long long>(a.M) * a.N,
+                        __bfloat16_as_ushort(__float2bfloat16_rn(o[i])));
             }
           }
         }
@@ -593,9 +605,11 @@ struct Fp8RowsCfg {
 struct Fp8Scales {
   float f0, f1, f2, f3;
   float4 x, w;  // the next group, as loaded
-  __device__ __forceinline__ void load4(const float* px, const float* pw) {
-    x = __ldcg(reinterpret_cast<const float4*>(px));
-    w = __ldcg(reinterpret_cast<const float4*>(pw));
+  // four of each, from arrays of nx elements from bx and nw from bw
+  __device__ __forceinline__ void load4(const float* px, const float* bx, unsigned long long nx,
+                                        const float* pw, const float* bw, unsigned long long nw) {
+    x = ld_in<float4>(px, bx, nx);
+    w = ld_in<float4>(pw, bw, nw);
   }
   __device__ __forceinline__ void take() {
     f0 = x.x * w.x;
@@ -746,13 +760,17 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks)
     Fp8Scales sc;
     // aligned rows: groups of the row's own fours; else from the first block on
     const int ph = a.vec_s ? k0 & 3 : 0;
+    const unsigned long long n_sx = static_cast<unsigned long long>(a.M) * a.KB;
+    const unsigned long long n_sw = static_cast<unsigned long long>((a.N + 127) / 128) * a.KB;
+    const auto x1 = [&](int i) { return ld_in<float>(sxp + i, a.sx, n_sx); };
+    const auto w1 = [&](int i) { return ld_in<float>(swp + i, a.sw, n_sw); };
     auto request = [&](int i) {  // the group that starts with block i of this range
       if (a.vec_s) {
-        sc.load4(sxp + i, swp + i);
+        sc.load4(sxp + i, a.sx, n_sx, swp + i, a.sw, n_sw);
       } else {
         const int i1 = min(i + 1, n - 1), i2 = min(i + 2, n - 1), i3 = min(i + 3, n - 1);
-        sc.x = make_float4(__ldcg(sxp + i), __ldcg(sxp + i1), __ldcg(sxp + i2), __ldcg(sxp + i3));
-        sc.w = make_float4(__ldcg(swp + i), __ldcg(swp + i1), __ldcg(swp + i2), __ldcg(swp + i3));
+        sc.x = make_float4(x1(i), x1(i1), x1(i2), x1(i3));
+        sc.w = make_float4(w1(i), w1(i1), w1(i2), w1(i3));
       }
     };
     grid_dep_wait();
@@ -834,13 +852,14 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks)
       }
       const int col = nt * 128 + c;
       uint16_t* y = a.Y + static_cast<size_t>(r) * a.N + col;
+      const unsigned long long n_y = static_cast<unsigned long long>(a.M) * a.N;
       if (a.vec && col + 4 <= a.N) {
-        *reinterpret_cast<uint2*>(y) = make_uint2(bf16_pack2(sum.x, sum.y), bf16_pack2(sum.z, sum.w));
+        st_in(y, a.Y, n_y, make_uint2(bf16_pack2(sum.x, sum.y), bf16_pack2(sum.z, sum.w)));
       } else {
         const float s4[4] = {sum.x, sum.y, sum.z, sum.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          if (col + j < a.N) y[j] = __bfloat16_as_ushort(__float2bfloat16_rn(s4[j]));
+          if (col + j < a.N) st_in(y + j, a.Y, n_y, __bfloat16_as_ushort(__float2bfloat16_rn(s4[j])));
       }
     }
   }

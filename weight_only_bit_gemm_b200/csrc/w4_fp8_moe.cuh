@@ -93,12 +93,13 @@ __global__ void __launch_bounds__(256) moe_route_kernel(const MoeArgs a) {
     const int m = live ? b / a.HB : 0, k = (b - m * a.HB) * kFp8Block + l * 8;
     const bool have = live && k < a.H;
     const size_t at = static_cast<size_t>(m) * a.H + k;
-    const uint4 w = have ? __ldcg(reinterpret_cast<const uint4*>(a.X + at)) : make_uint4(0u, 0u, 0u, 0u);
+    const unsigned long long n_x = static_cast<unsigned long long>(a.T) * a.H;
+    const uint4 w = have ? ld_in<uint4>(a.X + at, a.X, n_x) : make_uint4(0u, 0u, 0u, 0u);
     float v[8];  // negated
     unpack_neg_bf16x8(w, v);
     const float sc = fp8_scale(half_warp_max(abs_max_bf16x8(w)));
-    if (have) *reinterpret_cast<uint2*>(a.xq + at) = fp8_codes8_neg(v, sc);
-    if (live && l == 0) a.sx[b] = sc;
+    if (have) st_in(a.xq + at, a.xq, n_x, fp8_codes8_neg(v, sc));
+    if (live && l == 0) st_in(a.sx + b, a.sx, static_cast<unsigned long long>(a.T) * a.HB, sc);
     return;
   }
 
@@ -116,7 +117,8 @@ __global__ void __launch_bounds__(256) moe_route_kernel(const MoeArgs a) {
       uint4 rw[8];
 #pragma unroll
       for (int c = 0; c < 8; ++c)
-        rw[c] = k + c * 256 < a.H ? __ldcg(reinterpret_cast<const uint4*>(r + k + c * 256))
+        rw[c] = k + c * 256 < a.H ? ld_in<uint4>(r + k + c * 256, a.router,
+                                                 static_cast<unsigned long long>(a.E) * a.H)
                                   : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
       for (int i = 0; i < kMoeRouteTokens; ++i) {
@@ -125,7 +127,8 @@ __global__ void __launch_bounds__(256) moe_route_kernel(const MoeArgs a) {
 #pragma unroll
         for (int c = 0; c < 8; ++c)
           xw[c] = k + c * 256 < a.H
-                      ? __ldcg(reinterpret_cast<const uint4*>(x + static_cast<size_t>(i) * a.H + k + c * 256))
+                      ? ld_in<uint4>(x + static_cast<size_t>(i) * a.H + k + c * 256, a.X,
+                                     static_cast<unsigned long long>(a.T) * a.H)
                       : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
@@ -141,15 +144,17 @@ __global__ void __launch_bounds__(256) moe_route_kernel(const MoeArgs a) {
     for (int i = 0; i < kMoeRouteTokens; ++i) {
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) d[i] += __shfl_xor_sync(0xffffffffu, d[i], o);
-      if (lane == 0 && t0 + i < a.T) a.logits[static_cast<size_t>(t0 + i) * a.E + e] = d[i];
+      if (lane == 0 && t0 + i < a.T)
+        st_in(a.logits + static_cast<size_t>(t0 + i) * a.E + e, a.logits,
+              static_cast<unsigned long long>(a.T) * a.E, d[i]);
     }
   }
   // (the barrier and thread 0's acquire-release publish the CTA's logits and
   // make the other CTAs' visible)
   __syncthreads();
   if (threadIdx.x == 0) {
-    last = eg == 1 ||
-                   atom_add_acq_rel_gpu(&a.cnt->group[tg], 1u) == static_cast<unsigned>(eg - 1)
+    last = eg == 1 || (in_bounds(tg, kMoeMaxTokens / kMoeRouteTokens) &&
+                       atom_add_acq_rel_gpu(&a.cnt->group[tg], 1u) == static_cast<unsigned>(eg - 1))
                ? 1 : 0;
     if (last && eg > 1) a.cnt->group[tg] = 0u;
   }
@@ -166,7 +171,9 @@ __global__ void __launch_bounds__(256) moe_route_kernel(const MoeArgs a) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int x = i * 32 + lane;
-      v[i] = x < a.E ? __ldcg(a.logits + static_cast<size_t>(t) * a.E + x) : 0.0f;
+      v[i] = x < a.E ? ld_in<float>(a.logits + static_cast<size_t>(t) * a.E + x, a.logits,
+                                    static_cast<unsigned long long>(a.T) * a.E)
+                     : 0.0f;
       key[i] = x < a.E ? moe_key(v[i]) : 0u;
     }
     int pick = 0;       // lane j keeps choice j
@@ -215,8 +222,8 @@ __global__ void __launch_bounds__(256) moe_route_kernel(const MoeArgs a) {
       total = mine;
     }
     if (lane < a.top) {
-      a.ids[t * a.top + lane] = pick;
-      a.weights[t * a.top + lane] = weight / total;
+      st_in(a.ids + t * a.top + lane, a.ids, static_cast<unsigned>(a.T * a.top), pick);
+      st_in(a.weights + t * a.top + lane, a.weights, static_cast<unsigned>(a.T * a.top), weight / total);
     }
   }
   __syncthreads();
@@ -235,7 +242,10 @@ __global__ void __launch_bounds__(256) moe_route_kernel(const MoeArgs a) {
   for (int i = threadIdx.x; i < a.E; i += 256) flags[i] = 0u;
   __syncthreads();
   const int pairs = a.T * a.top;
-  for (int i = threadIdx.x; i < pairs; i += 256) flags[__ldcg(a.ids + i)] = 1u;
+  for (int i = threadIdx.x; i < pairs; i += 256) {
+    const int e = __ldcg(a.ids + i);
+    if (in_bounds(e, a.E)) flags[e] = 1u;
+  }
   __syncthreads();
   if (warp == 0) {
     int base = 0;
@@ -255,10 +265,14 @@ __global__ void __launch_bounds__(256) moe_route_kernel(const MoeArgs a) {
     }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < last * a.T; i += 256) a.wt[i] = -1.0f;
+  const unsigned n_wt = static_cast<unsigned>(a.A * a.T);
+  for (int i = threadIdx.x; i < last * a.T; i += 256) st_in(a.wt + i, a.wt, n_wt, -1.0f);
   __syncthreads();
-  for (int i = threadIdx.x; i < pairs; i += 256)
-    a.wt[static_cast<size_t>(slot[__ldcg(a.ids + i)]) * a.T + i / a.top] = __ldcg(a.weights + i);
+  for (int i = threadIdx.x; i < pairs; i += 256) {
+    const int e = __ldcg(a.ids + i);
+    if (in_bounds(e, a.E))
+      st_in(a.wt + static_cast<size_t>(slot[e]) * a.T + i / a.top, a.wt, n_wt, __ldcg(a.weights + i));
+  }
 }
 
 // ------------------------------------------------------------------ experts
@@ -277,6 +291,12 @@ __device__ __forceinline__ void fence_proxy_async_all() {
 }
 __device__ __forceinline__ void st_cluster_u32(uint32_t cluster_addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
+}
+
+// The expert of active slot i.
+__device__ __forceinline__ int moe_expert(const MoeArgs& a, int i) {
+  const int e = ld_in<int>(a.active + 1 + i, a.active, a.A + 1);
+  return in_bounds(e, a.E) ? e : 0;
 }
 
 // Bounded wait until every gate and up CTA has published its part of h.
@@ -323,11 +343,19 @@ __device__ __forceinline__ void moe_block_sums(const MoeArgs& a, const MoeBlocks
   const float* pb = q.pb;
   int act = q.act, kb = q.k0, left = q.n;  // of the next group to request
   float w_next = 1.0f;
+  // the arrays behind pa and pb, and their extents
+  const float* ba = UP ? a.sx : a.sh;
+  const float* bb = UP ? a.s13 : a.s2;
+  const unsigned long long na =
+      UP ? static_cast<unsigned long long>(a.T) * a.HB : static_cast<unsigned long long>(a.A) * a.T * a.IB;
+  const unsigned long long nb = static_cast<unsigned long long>(UP ? 2 * a.E : a.E) * a.IB * a.HB;
   auto enter = [&]() {
-    w_next = __ldcg(a.wt + act * a.T + t);
+    w_next = ld_in<float>(a.wt + act * a.T + t, a.wt, static_cast<unsigned>(a.A * a.T));
     pa = a.sh + (static_cast<size_t>(act) * a.T + t) * a.IB;
-    pb = a.s2 + (static_cast<size_t>(__ldcg(a.active + 1 + act)) * a.HB + q.nt) * a.IB;
+    pb = a.s2 + (static_cast<size_t>(moe_expert(a, act)) * a.HB + q.nt) * a.IB;
   };
+  const auto a1 = [&](int k) { return ld_in<float>(pa + k, ba, na); };
+  const auto b1 = [&](int k) { return ld_in<float>(pb + k, bb, nb); };
   if (!UP) enter();
   Fp8Scales sc;
   float w = 1.0f, w_req = 1.0f;    // of the current group, of the requested one
@@ -346,11 +374,11 @@ __device__ __forceinline__ void moe_block_sums(const MoeArgs& a, const MoeBlocks
     if (!UP && w_next < 0.0f) {
       sc.x = sc.w = make_float4(0.f, 0.f, 0.f, 0.f);
     } else if (vec) {
-      sc.load4(pa + (kb & ~3), pb + (kb & ~3));
+      sc.load4(pa + (kb & ~3), ba, na, pb + (kb & ~3), bb, nb);
     } else {
       const int k1 = min(kb + 1, len - 1), k2 = min(kb + 2, len - 1), k3 = min(kb + 3, len - 1);
-      sc.x = make_float4(__ldcg(pa + kb), __ldcg(pa + k1), __ldcg(pa + k2), __ldcg(pa + k3));
-      sc.w = make_float4(__ldcg(pb + kb), __ldcg(pb + k1), __ldcg(pb + k2), __ldcg(pb + k3));
+      sc.x = make_float4(a1(kb), a1(k1), a1(k2), a1(k3));
+      sc.w = make_float4(b1(kb), b1(k1), b1(k2), b1(k3));
     }
     kb += have_req;
     left -= have_req;
@@ -482,7 +510,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks)
   int expert = 0, slot = 0, ib = 0, half64 = 0, k0 = 0, nt = 0;
   if (up) {
     slot = ticket / per_expert;
-    expert = __ldcg(a.active + 1 + slot);
+    expert = moe_expert(a, slot);
     ib = (ticket - slot * per_expert) * per + rank / group;
     half64 = rank % group / a.ksplit;
     const int s = rank % a.ksplit;
@@ -514,7 +542,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks)
         } else {
           const int act = (k0 + i) / a.IB;
           tma_load_3d(ws + s * C::kWStage, &w2map, (k0 + i - act * a.IB) * 128, nt * 128,
-                      __ldcg(a.active + 1 + act), &full[s], pol_w);
+                      moe_expert(a, act), &full[s], pol_w);
         }
       };
       auto load_x = [&](int i) {
@@ -608,7 +636,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks)
     const uint32_t mine = smem_u32(sums);
     if (ib < a.IB) {
       for (int t = (rank - g0) * C::kWarps + warp; t < a.T; t += group * C::kWarps) {
-        if (__ldcg(a.wt + slot * a.T + t) < 0.0f) continue;
+        if (ld_in<float>(a.wt + slot * a.T + t, a.wt, static_cast<unsigned>(a.A * a.T)) < 0.0f) continue;
         const int owner = g0 + (lane >> 4) * a.ksplit;
         const uint32_t at = mine + static_cast<uint32_t>(t * C::kRow + (lane & 15) * 4) * 4u;
         float4 g = make_float4(0.f, 0.f, 0.f, 0.f), u = g;
@@ -630,11 +658,12 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks)
         const float sc = fp8_scale(mx);
         const size_t hrow = static_cast<size_t>(slot) * a.T + t;
         const int c = ib * kFp8Block + lane * 4;
-        if (c < a.I && in_bounds(hrow * a.I + c + 3, static_cast<unsigned long long>(a.A) * a.T * a.I))
-          *reinterpret_cast<uint32_t*>(a.hq + hrow * a.I + c) =
-              e4m3x2(__fdiv_rn(h[0], sc), __fdiv_rn(h[1], sc)) |
-              (e4m3x2(__fdiv_rn(h[2], sc), __fdiv_rn(h[3], sc)) << 16);
-        if (lane == 0) a.sh[hrow * a.IB + ib] = sc;
+        const unsigned long long rows = static_cast<unsigned long long>(a.A) * a.T;
+        if (c < a.I)
+          st_in(a.hq + hrow * a.I + c, a.hq, rows * a.I,
+                e4m3x2(__fdiv_rn(h[0], sc), __fdiv_rn(h[1], sc)) |
+                    (e4m3x2(__fdiv_rn(h[2], sc), __fdiv_rn(h[3], sc)) << 16));
+        if (lane == 0) st_in(a.sh + hrow * a.IB + ib, a.sh, rows * a.IB, sc);
       }
     }
     // publish: ordinary stores, read elsewhere by tensor copies and loads
@@ -664,13 +693,14 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks)
       }
       const int col = nt * 128 + c;
       uint16_t* y = a.Y + static_cast<size_t>(r) * a.H + col;
+      const unsigned long long n_y = static_cast<unsigned long long>(a.T) * a.H;
       if (a.vec && col + 4 <= a.H) {
-        *reinterpret_cast<uint2*>(y) = make_uint2(bf16_pack2(sum.x, sum.y), bf16_pack2(sum.z, sum.w));
+        st_in(y, a.Y, n_y, make_uint2(bf16_pack2(sum.x, sum.y), bf16_pack2(sum.z, sum.w)));
       } else {
         const float s4[4] = {sum.x, sum.y, sum.z, sum.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          if (col + j < a.H) y[j] = __bfloat16_as_ushort(__float2bfloat16_rn(s4[j]));
+          if (col + j < a.H) st_in(y + j, a.Y, n_y, __bfloat16_as_ushort(__float2bfloat16_rn(s4[j])));
       }
     }
   }
