@@ -451,7 +451,10 @@ w4_status fp4_gemm(const uint16_t* X, const uint8_t* Wp, const float* s2, int M,
  *                KB = ceil(K / 128)
  *   weights      one scale per 128 x 128 block, sw [ceil(N / 128), KB]
  *   s = fp32(max|v over the block| / 448) (1 if that is 0)
- *   q = e4m3_rne(fp32(v / s))                           (IEEE divisions)
+ *   q = e4m3_rne(fp32(v / s)), at most 448 in magnitude (IEEE divisions)
+ * A rounding of s can leave |v / s| above 448, by 2^-23 of it where s is normal;
+ * below 2^-126, where s has few bits, by more (largest |v| 600 * 2^-149: s is
+ * 2^-149).  The code is that of 448 then.
  * Blocks start at row and channel 0; the last of a row or column may be
  * shorter.  K % 16 == 0 everywhere.  A block that holds an infinity or a NaN
  * gets the scale NaN and NaN codes, so every product with it is NaN.
@@ -487,7 +490,7 @@ w4_status fp8_add_rmsnorm(const uint16_t* X, const uint16_t* residual, const uin
 
 /* Y[m,n] = bf16_rne( sum_j sx[m,j] sw[n/128,j] sum_{k in block j} qx[m,k] qw[n,k] ),
  * j over the 128-channel blocks; fp32 sums (the products of two codes are
- * exact).
+ * exact).  sx sw is rounded to fp32 first, so it has to lie in fp32's range.
  *   qx, sx     in   e4m3 [M, K] (16-byte aligned), fp32 [M, KB]
  *   qw, sw     in   e4m3 [N, K] (16-byte aligned), fp32 [ceil(N / 128), KB]
  *   M, N, K    M, N <= 2^24, K <= 2^20, M K and N K < 2^40, M N < 2^39: larger

@@ -4,6 +4,7 @@ import gc
 import types
 import weakref
 
+import numpy as np
 import pytest
 import torch
 
@@ -11,6 +12,8 @@ from weight_only_bit_gemm_b200 import build
 
 build.build()
 from weight_only_bit_gemm_b200 import w4  # noqa: E402
+
+import oracle as O  # noqa: E402
 
 F8 = torch.float8_e4m3fn
 STREAM = 7
@@ -74,3 +77,18 @@ def test_default_workspaces_given_up_after_a_call_that_did_not_run_through(host,
     assert w4.device_status() == getattr(w4, status)
     lost = status in ("W4_ERR_TIMEOUT", "W4_ERR_BOUNDS")
     assert sorted(w4._FP8_WS) == ([(1, 5)] if lost else [(0, 5), (0, 6), (1, 5)])
+
+
+@pytest.mark.parametrize("units", [224, 225, 300, 600, 671, 672, 1000])
+def test_oracle_saturates_where_the_scale_is_subnormal(units):
+    # the largest value in units of 2^-149: its scale is rounded to a whole
+    # number of them, and a quotient past 448 has the code of 448
+    w = np.zeros((2, 16), np.float32)
+    w[0, :3] = np.array([units, -units, units // 2]) * 2.0 ** -149
+    q, s = O.fp8_quantize_blocks(w)
+    scale = int(np.rint(units / 448))
+    assert s[0, 0] == (np.float32(scale * 2.0 ** -149) if scale else np.float32(1))
+    top = O.e4m3_codes(np.array([min(units / scale, 448.0) if scale else 0.0]))[0]
+    assert q[0, 0] == top and q[0, 1] == (top | 0x80)
+    if units in (600, 671):
+        assert top == 0x7E

@@ -271,3 +271,21 @@ def test_vectors_written_on_the_stream(w4, call):
     torch.cuda.synchronize()
     ok(w4)
     assert [t for t, y in enumerate(got) if not torch.equal(y, alone[t & 1])] == []
+
+
+# ------------------------------------------------------- the smallest blocks
+
+def test_weight_blocks_with_subnormal_scales(w4):
+    # one block per largest value, in units of 2^-149
+    units = [1, 223, 224, 225, 300, 448, 600, 671, 672, 1000, 5000, 10 ** 6, 2 ** 23, 2 ** 25]
+    rng = np.random.default_rng(11)
+    W = np.concatenate([np.rint(rng.uniform(-u, u, (16, 128))) * 2.0 ** -149 for u in units], axis=1)
+    W = W.astype(np.float32)
+    for i, u in enumerate(units):
+        W[i % 16, 128 * i + 5] = -u * 2.0 ** -149
+        W[(i + 3) % 16, 128 * i + 77] = u * 2.0 ** -149
+    q, s = w4.fp8_quantize_weights(dev(W))
+    ok(w4)
+    qr, sr = O.fp8_quantize_blocks(W)
+    assert np.array_equal(codes(q), qr)
+    same_scales(s.cpu().numpy(), sr)

@@ -6,8 +6,9 @@
 //   s = max|v over the block| / 448   (IEEE division; 1 if that is 0)
 //   q = e4m3_rne(fp32(v / s))
 //
-// 448 is e4m3's largest value, so |v / s| <= 448 (1 + 2^-23) and nothing
-// saturates to anything but 448.  The maximum is taken on the bit patterns of
+// 448 is e4m3's largest value.  Where s is normal |v / s| <= 448 (1 + 2^-23),
+// which rounds to 448; a subnormal s has few bits, the quotient can be up to 671,
+// and the code saturates at 448.  The maximum is taken on the bit patterns of
 // |v| as integers, whose order puts infinity and NaN above every finite value:
 // a block that holds one gets the scale NaN and NaN codes, so a product with
 // it is NaN instead of silently losing the value.
