@@ -535,6 +535,10 @@ w4_status fp8_moe(const uint16_t* X, const uint16_t* router, const uint8_t* w13,
                   int renormalize, uint16_t* Y, int32_t* ids, float* weights, void* workspace,
                   size_t workspace_bytes, w4_stream stream);
 
+/* As w4_selftest_wait_timeout, for the expert kernel's wait on the counter that
+ * publishes h.                                                              */
+w4_status fp8_selftest_wait_timeout(w4_stream stream);
+
 #ifdef __cplusplus
 }
 #endif

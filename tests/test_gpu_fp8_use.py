@@ -97,15 +97,16 @@ def test_two_host_threads_on_one_stream(w4, own_workspace):
 
 # ------------------------------------------------- after a wait that gave up
 
-def test_calls_after_a_timeout(w4):
-    # a wait has run out (the short one of the self-test): whatever the default
+@pytest.mark.parametrize("wait", ["selftest_wait_timeout", "fp8_selftest_wait_timeout"])
+def test_calls_after_a_timeout(w4, wait):
+    # a wait has run out (the short one of a self-test): whatever the default
     # workspaces' counters hold then, the next calls do not start from it
     args = moe_tensors(draw_moe(5, 6, 400, 144, 63))
     alone = w4.fp8_moe(*args, 2)
     ok(w4)
     here = (torch.cuda.current_device(), torch.cuda.current_stream().cuda_stream)
     w4._FP8_WS[here].fill_(1)
-    w4.selftest_wait_timeout()
+    getattr(w4, wait)()
     assert w4.device_status() == w4.W4_ERR_TIMEOUT
     assert here not in w4._FP8_WS       # (else the next line must not run)
     again = w4.fp8_moe(*args, 2)

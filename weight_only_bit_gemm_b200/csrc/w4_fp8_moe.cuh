@@ -299,11 +299,12 @@ __device__ __forceinline__ int moe_expert(const MoeArgs& a, int i) {
   return in_bounds(e, a.E) ? e : 0;
 }
 
-// Bounded wait until every gate and up CTA has published its part of h.
-__device__ __forceinline__ bool moe_wait_h(const MoeArgs& a, unsigned want) {
+// Bounded wait until a counter in global memory has reached `want`.
+__device__ __forceinline__ bool wait_counter(const unsigned int* counter, unsigned want,
+                                             long long limit = kWaitLimitCycles) {
   const long long t0 = clock64();
-  while (ld_acquire_gpu(&a.cnt->h_done) < want) {
-    if (clock64() - t0 > kWaitLimitCycles) {
+  while (ld_acquire_gpu(counter) < want) {
+    if (clock64() - t0 > limit) {
       set_dev_error(W4_DEV_ERR_TIMEOUT);
       return false;
     }
@@ -311,6 +312,15 @@ __device__ __forceinline__ bool moe_wait_h(const MoeArgs& a, unsigned want) {
   }
   return true;
 }
+// ... until every gate and up CTA has published its part of h.
+__device__ __forceinline__ bool moe_wait_h(const MoeArgs& a, unsigned want) {
+  return wait_counter(&a.cnt->h_done, want);
+}
+
+// Failure-path check: the wait on a counter that nothing raises, with a short
+// limit (about 1 ms).
+__device__ unsigned int g_idle_counter;
+__global__ void counter_timeout_probe_kernel(long long limit) { wait_counter(&g_idle_counter, 1u, limit); }
 
 // What an epilogue warp needs for a CTA's run of blocks.
 struct MoeBlocks {

@@ -75,6 +75,7 @@ _SIGS = {
     "fp8_add_rmsnorm": (_i, [_p, _p, _p, ctypes.c_float, _i, _i, _p, _p, _p, _p, _p]),
     "fp8_gemm_workspace_bytes": (_sz, [_i, _i, _i]),
     "fp8_gemm": (_i, [_p, _p, _p, _p, _i, _i, _i, _p, _p, _sz, _p]),
+    "fp8_selftest_wait_timeout": (_i, [_p]),
     "fp8_moe_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
     "fp8_moe": (_i, [_p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _p, _p, _p, _p, _sz, _p]),
 }
@@ -177,6 +178,11 @@ def selftest_wait_timeout() -> None:
     """Run the bounded-wait failure path once (see w4.h); device_status() then
     reports W4_ERR_TIMEOUT."""
     _check(lib.w4_selftest_wait_timeout(_stream()), "w4_selftest_wait_timeout")
+
+
+def fp8_selftest_wait_timeout() -> None:
+    """The same for the expert layer's wait on a counter in global memory."""
+    _check(lib.fp8_selftest_wait_timeout(_stream()), "fp8_selftest_wait_timeout")
 
 
 # ----------------------------------------------------------------- INT4 RTN
