@@ -477,6 +477,9 @@ w4_status fp8_quantize_activations(const uint16_t* X, int M, int K, uint8_t* qx,
  *   residual_out = bf16_rne(r), Y = bf16_rne(y),
  *   (qy, sy) = codes and scales of y as fp8_quantize_activations defines them,
  *   from the unrounded y
+ * A row whose squares or their sum leave fp32's range is not normalised: past it
+ * the finite values become 0; where all squares round to 0 and eps = 0, infinite
+ * or NaN.
  *   X             in   bf16 [M, K];  K <= 65536 (else W4_ERR_UNSUPPORTED)
  *   residual      in   bf16 [M, K] or NULL (r = X)
  *   weight        in   bf16 [K];  eps >= 0
@@ -497,12 +500,12 @@ w4_status fp8_add_rmsnorm(const uint16_t* X, const uint16_t* residual, const uin
  *              returns W4_ERR_UNSUPPORTED, launching nothing
  *   Y          out  bf16 [M, N]
  *   workspace  at least fp8_gemm_workspace_bytes(M, N, K) bytes (0 for an
- *              invalid or unsupported shape), 256-byte aligned, ZEROED ONCE before its first
- *              use; the call leaves its counters (the first 262144 bytes)
- *              zeroed, so calls of any shape, and w4a16_gemm / nf4_gemm, may
- *              share it as long as they are ordered on one stream, from
- *              whichever host threads.  After W4_ERR_TIMEOUT it must be
- *              zeroed again.
+ *              invalid or unsupported shape), 256-byte aligned, ZEROED ONCE
+ *              before its first use; the call leaves its counters (the first
+ *              262144 bytes) zeroed, so calls of any shape, and w4a16_gemm /
+ *              nf4_gemm, may share it as long as they are ordered on one
+ *              stream, from whichever host threads.  After W4_ERR_TIMEOUT it
+ *              must be zeroed again.
  * Everything is read in the stream's order, the weights too (unlike Wp in
  * w4a16_gemm): qw and sw may be written by any kernel ahead of the call.    */
 size_t fp8_gemm_workspace_bytes(int M, int N, int K);
@@ -527,8 +530,10 @@ w4_status fp8_gemm(const uint8_t* qx, const float* sx, const uint8_t* qw, const 
  *   Y          out  bf16 [T, H];  ids  out  int32 [T, top];  weights  out  fp32 [T, top]
  *   workspace  as for fp8_gemm, fp8_moe_workspace_bytes(T, E, top, H, I) bytes
  * T, E, top, H or I above the limits: W4_ERR_UNSUPPORTED (workspace size 0).
- * X, router, w13, w2 are 16-byte aligned.  More tokens: fp8_gemm per expert.  A token whose logits are all NaN is given experts
- * 0..top-1 and a NaN output.                                                */
+ * X, router, w13, w2 are 16-byte aligned.  More tokens: fp8_gemm per expert.  A
+ * token whose logits are all NaN is given experts 0..top-1 and a NaN output.
+ * The call's two kernels follow each other on the stream, whichever other host
+ * threads use it.                                                           */
 size_t fp8_moe_workspace_bytes(int T, int E, int top, int H, int I);
 w4_status fp8_moe(const uint16_t* X, const uint16_t* router, const uint8_t* w13, const float* s13,
                   const uint8_t* w2, const float* s2, int T, int E, int top, int H, int I,

@@ -153,9 +153,11 @@ __device__ __forceinline__ uint32_t abs_max_bf16x8(uint4 w) {
 // Half a warp per (token, 128 channels): 8 channels per lane, one 16-byte
 // load and one 8-byte store, U blocks in flight.  K % 16 == 0; with RAGGED the
 // last block of a row is shorter (lanes past K hold nothing), without it the
-// blocks are simply consecutive.  Bound by instruction issue: 4099 x 13824 in
-// 40 us, 4.3 TB/s (with one-wide fp32 arithmetic and U = 2 45 us, U = 1 53 us,
-// U = 4 58 us).
+// blocks are simply consecutive.  4099 x 13824 in 40 us, 4.3 TB/s.  Bound by
+// instruction issue first: 17.5 instructions per value are 28 us of it (profile);
+// then by the loads' latency, with 5 CTAs per SM (46 registers) and no load
+// in flight while a turn's codes are made.  (One-wide fp32 arithmetic and U = 2
+// 45 us, U = 1 53 us, U = 4 58 us.)
 template <int U, bool RAGGED>
 __global__ void __launch_bounds__(256)
     fp8_quantize_x_kernel(const uint16_t* X, long long blocks, int K, FastDivIdx by_kb, uint8_t* q,
@@ -200,8 +202,10 @@ constexpr int kFp8WThreads = 256, kFp8WBlocks = 3;
 
 // One CTA per 128 x 128 block of one of B matrices: 16 lanes per row, 8
 // channels per lane, 16 rows at a time; the values stay in registers between
-// the maximum and the codes.  Bound by HBM: 16 x 2000 x 4096 in 115 us, 5.7 TB/s
-// (2 CTAs per SM 126 us; CTAs of 512 threads, 2 per SM, 119 us).
+// the maximum and the codes.  Bound by HBM: 16 x 2000 x 4096 in 106 us, 6.2 TB/s;
+// a single matrix of 4096 x 4096, 17 us, by 1024 CTAs on 444 places.  Three CTAs
+// per SM leave 80 registers, 28 bytes short (they spill to the stack); 2 CTAs
+// per SM, or CTAs of 512 threads, 2 per SM, were slower by 10 % and 3 %.
 __global__ void __launch_bounds__(kFp8WThreads, kFp8WBlocks)
     fp8_quantize_w_kernel(const float* W, int N, int K, uint8_t* q, float* s,
                           unsigned long long values) {  // B N K
@@ -257,8 +261,9 @@ __global__ void __launch_bounds__(kFp8WThreads, kFp8WBlocks)
 // y = r * rsqrt(mean + eps) * w in fp32 and its codes without a rounding in
 // between.  residual_out is bf16(r); the norm itself uses the unrounded sum.
 // Every thread reads its own channels before it writes them, so residual_out
-// may be residual or x.  Bound by HBM: 8191 x 8192 with every output in 97
-// us, 6.2 TB/s; one row of 4096 in 2.4 us, the launch.
+// may be residual or x.  Bound by HBM: 8191 x 8192 with every output in 100 to
+// 106 us, 5.7 to 6.1 TB/s; one row of 4096 in 2.4 us, the launch.  Above 32768
+// channels a thread's 64 values spill in part (224 bytes).
 // Up to 16384 channels a thread has 32 registers, which fills an SM with threads;
 // left to itself the compiler's choice moves with small changes (50 registers:
 // 8191 x 8192 in 129 us).

@@ -24,15 +24,19 @@
 // More tokens (fp8_tc_gemm_kernel): CTA pairs (cta_group::2) of 256 tokens x
 // 256 or 128 weight rows, each CTA staging half of each operand, in a
 // persistent grid.  Each pair takes whole tiles while every pair gets one; the
-// tiles left over stay whole or are cut along K into equal runs of blocks, whose fp32 partial sums the last run of a tile
-// to finish adds in the order of K (the result does not depend on which
-// that is).
+// tiles left over stay whole or are cut along K into equal runs of blocks, whose
+// fp32 partial sums the last run of a tile to finish adds in the order of K (the
+// result does not depend on which that is).
 //
-// Measured on B200 (time per call in a graph): 1 x 12288 x 4096 12.1 us, 4.2
-// TB/s; 1 x 16384 x 16384 43 us, 6.2 TB/s; 2048 x 28672 x 8192 466 to 498 us,
-// 1.93 to 2.06 PFLOP/s, where a pair's block takes 0.56 us: bound by the
-// hand-over of the two accumulator buffers (0.50 us with no loads) and by the
-// operands' way through L2 (0.456 us with no read-out).
+// Measured on B200, per call.  Up to 64 tokens about 5.5 us that do not depend on
+// K, then the weights: 1 x 12288 x 4096 12.5 us, 4.0 TB/s; 33 x 4096 x 11008
+// 14.5 us (5.3 TB/s for what K adds).  128 x 12288 x 4096 18.2 us: 96 tiles on
+// 148 SMs, 0.41 us per block of a CTA.  2048 x 28672 x 8192 470 to 515 us (1.87
+// to 2.05 PFLOP/s) in short runs, 550 us (1.75 PFLOP/s) in a loop of seconds,
+// where the 1000 W limit takes the SMs to 1.57 GHz.  A pair's block takes 0.56 us:
+// bound by the hand-over of the two accumulator buffers (0.50 us with no loads)
+// and by the operands' way through L2 (0.456 us with no read-out).  With 256
+// weight rows the epilogue warps' 128 running sums leave 44 bytes on the stack.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -574,8 +578,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
 // QUADS: tensor-memory lane quadrants in use (32 tokens each).  With fewer than
 // 4 the MMA's other rows are whatever follows the token rows in shared memory
 // (inside it: the weight stages), and their sums are never read.  Up to 64
-// tokens two CTAs fit on an SM, so that the next call's stream their first
-// weights while this one's finish.
+// tokens two CTAs fit on an SM, so that the next call's set up and bring their
+// first weights into L2 while this one's finish.
 template <int QUADS_, int STAGES_>
 struct Fp8RowsCfg {
   static constexpr int QUADS = QUADS_;
