@@ -278,8 +278,10 @@ w4_status w4_unprepack(const uint8_t* Wp, int N, int K, int G, int act_order,
  * of 64..256 tokens.  The kernels use programmatic dependent launch and
  * start reading Wp before the kernel before them on the stream has
  * finished: Wp is constant model state and must not be written by that
- * kernel (this library's prepack kernels make their writes visible before
- * they exit, so prepack followed by a GEMM is fine).
+ * kernel, nor by one further ahead that may not have ended when the kernel
+ * between started (the fp8_* calls and this library's GEMMs start so).  The
+ * prepack kernels make their writes visible before they exit, so prepack
+ * followed by a GEMM is fine.
  *   X          in   bf16 [M, K], 16-byte aligned, K % 64 == 0
  *   Wp         in   from w4_prepack (act_order must match)
  *   M, N, K, G M >= 1, N >= 1; with M <= 32 (the decode kernel) N is at most
